@@ -27,6 +27,8 @@ __all__ = [
     "swiglu_quantize",
     "hadamard32_quantize", "quantize_dual", "gemm", "gemm_mxout", "linear_ws_bytes", "linear_fwd", "linear_dgrad",
     "linear_wgrad", "linear_fwd_save", "linear_bwd", "workspace", "check_device_status",
+    "layer_norm_fwd", "layer_norm_bwd", "dropout_fwd", "dropout_bwd",
+    "dropout_add_layer_norm_fwd", "dropout_add_layer_norm_bwd", "swiglu_bwd",
 ]
 
 MXFP4, NVFP4_GLOBAL, NVFP4_CTA, MXFP4_NOCLIP = 0, 1, 2, 3
@@ -73,6 +75,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     P, i64, u64, u32, sz, ci, f32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64,
                                      ctypes.c_uint32, ctypes.c_size_t, ctypes.c_int,
                                      ctypes.c_float)
+    f64 = ctypes.c_double
     PSZ = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "fa4_quant_sizes": [i64, i64, ci, ci, PSZ, PSZ, PSZ, PSZ],
@@ -96,6 +99,17 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         "fa4_debug_gemm_timeout": [_QT, _QT, i64, i64, i64, ci, P, i64, ci, u64, P, sz, P],
         "fa4_quantize_nvfp4_global_noalloc": [P, i64, i64, i64, ci, ci, u64, _QT, P],
         "fa4_swiglu_quantize": [P, i64, i64, i64, ci, ci, u64, _QT, ci, ci, u32, ci, u64, _QT, P],
+        "fa4_swiglu_bwd": [P, i64, P, i64, i64, i64, P, i64, P],
+        "fa4_layernorm_ws_bytes": [i64, i64, PSZ],
+        "fa4_layernorm_fwd": [P, i64, i64, i64, ci, P, P, ci, f32, ci, P, i64, P, P, P],
+        "fa4_layernorm_bwd": [P, i64, P, i64, P, i64, i64, i64, ci, P, ci, ci, P, P, P, i64, P, P,
+                              P, sz, P],
+        "fa4_dropout_fwd": [P, i64, P, i64, i64, i64, ci, f64, u64, P, P, i64, P],
+        "fa4_dropout_bwd": [P, i64, i64, i64, ci, f64, u64, P, P, i64, P],
+        "fa4_dropout_add_layernorm_fwd": [P, i64, P, i64, i64, i64, ci, f64, u64, P, P, P, ci, f32,
+                                          ci, P, i64, P, i64, P, P, P],
+        "fa4_dropout_add_layernorm_bwd": [P, i64, P, i64, P, i64, i64, i64, ci, f64, u64, P, P, ci,
+                                          ci, P, P, P, i64, P, i64, P, P, P, sz, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -564,3 +578,241 @@ def gemm_mxout(A: QTensor, B: QTensor, alpha: float = 1.0, store_d: bool = True,
                                             ldd, qout.c(), _ptr(ws), ws.numel(), _stream(dev)),
            "fa4_gemm_blockscaled_mxout")
     return (out if store_d else None), qout
+
+
+# ------------------------------------- training operators between the linears
+
+DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
+def _rows(x: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """The leading dimension of a 2-D CUDA matrix of one of the DTYPEs (with
+    `like`: of its shape, type and device)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or x.dtype not in DTYPE:
+        raise ValueError(f"{name} must be a 2-D bf16, fp16 or fp32 CUDA tensor")
+    if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
+        raise ValueError(f"{name} must be a {list(like.shape)} {like.dtype} tensor on {like.device}")
+    rows, cols = x.shape
+    if cols != 1 and x.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows == 1:
+        return -(-cols // 8) * 8  # one row: its stride means nothing
+    if x.stride(0) < cols:
+        raise ValueError(f"{name} has overlapping rows (row stride {x.stride(0)} < {cols})")
+    return x.stride(0)
+
+
+def _new_rows(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _vector(v: torch.Tensor, n: int, dtypes: tuple, device, name: str):
+    if not isinstance(v, torch.Tensor) or v.dtype not in dtypes or v.shape != (n,) or \
+            v.device != device or not v.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor of "
+                         f"{' or '.join(str(d) for d in dtypes)} on {device}")
+
+
+def _weights(weight, bias, x) -> int:
+    _vector(weight, x.shape[1], (x.dtype, torch.float32), x.device, "weight")
+    if bias is not None:
+        _vector(bias, x.shape[1], (weight.dtype,), x.device, "bias")
+    return DTYPE[weight.dtype]
+
+
+def _stats(mean, rstd, center, x):
+    _vector(rstd, x.shape[0], (torch.float32,), x.device, "rstd")
+    if center:
+        _vector(mean, x.shape[0], (torch.float32,), x.device, "mean")
+
+
+def _step(step, x):
+    if step is not None and (not isinstance(step, torch.Tensor) or step.dtype != torch.int64 or
+                             step.numel() != 1 or step.device != x.device):
+        raise ValueError(f"step must be a tensor of one int64 on {x.device}")
+    return _ptr(step)
+
+
+def _grads(dweight, dbias, bias_grad, x):
+    n, dev = x.shape[1], x.device
+    if dweight is None:
+        dweight = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector(dweight, n, (torch.float32,), dev, "dweight")
+    if not bias_grad:
+        return dweight, None
+    if dbias is None:
+        dbias = torch.empty(n, dtype=torch.float32, device=dev)
+    else:
+        _vector(dbias, n, (torch.float32,), dev, "dbias")
+    return dweight, dbias
+
+
+def layer_norm_ws_bytes(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().fa4_layernorm_ws_bytes(rows, cols, ctypes.byref(n)), "fa4_layernorm_ws_bytes")
+    return n.value
+
+
+def _norm_ws(ws, x):
+    if ws is None:  # nothing in it has to start at zero
+        return torch.empty(layer_norm_ws_bytes(*x.shape), dtype=torch.uint8, device=x.device)
+    if ws.device != x.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {x.device}")
+    return ws
+
+
+@_on_tensor_device
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                   eps: float = 1e-5, center: bool = True, out: torch.Tensor | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor]:
+    """(y, mean, rstd): the layer norm of each row of x[T, N] (bf16, fp16 or
+    fp32), with float32 statistics for the backward pass.  center=False is the
+    RMS form: no mean (None).  weight and bias are of x's type or float32.
+    out may be x."""
+    ldx = _rows(x, "x")
+    wd = _weights(weight, bias, x)
+    y = _new_rows(x) if out is None else out
+    ldy = _rows(y, "out", x)
+    T, N = x.shape
+    mean = torch.empty(T, dtype=torch.float32, device=x.device) if center else None
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check(lib().fa4_layernorm_fwd(_ptr(x), ldx, T, N, DTYPE[x.dtype], _ptr(weight), _ptr(bias), wd,
+                                   eps, 1 if center else 0, _ptr(y), ldy, _ptr(mean), _ptr(rstd),
+                                   _stream(x.device)), "fa4_layernorm_fwd")
+    return y, mean, rstd
+
+
+@_on_tensor_device
+def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                   mean: torch.Tensor | None, rstd: torch.Tensor, center: bool = True,
+                   bias_grad: bool = True, dres: torch.Tensor | None = None,
+                   dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
+                   dbias: torch.Tensor | None = None, ws: torch.Tensor | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor | None]:
+    """(dx, dweight, dbias): dx of layer_norm_fwd plus dres, the gradient that
+    reaches x by another way (the residual stream); dweight and dbias are
+    float32 sums over the rows in a fixed order (dbias None without
+    bias_grad)."""
+    ldx, lddy = _rows(x, "x"), _rows(dy, "dy", x)
+    wd = _weights(weight, None, x)
+    _stats(mean, rstd, center, x)
+    ldr = 0 if dres is None else _rows(dres, "dres", x)
+    dx = _new_rows(x) if dx is None else dx
+    lddx = _rows(dx, "dx", x)
+    dweight, dbias = _grads(dweight, dbias, bias_grad, x)
+    ws = _norm_ws(ws, x)
+    T, N = x.shape
+    _check(lib().fa4_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _ptr(dres), ldr, T, N,
+                                   DTYPE[x.dtype], _ptr(weight), wd, 1 if center else 0,
+                                   _ptr(mean) if center else None, _ptr(rstd), _ptr(dx), lddx,
+                                   _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel(),
+                                   _stream(x.device)), "fa4_layernorm_bwd")
+    return dx, dweight, dbias
+
+
+@_on_tensor_device
+def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None
+                ) -> torch.Tensor:
+    """[residual +] dropout(x) with a mask computed from (seed + step, row,
+    column) and never stored; kept values are scaled by the reciprocal of
+    their probability (p in steps of 2^-16).  step: one int64 on the device,
+    for graphs that draw a new mask at each replay.  out may be x or
+    residual."""
+    ldx = _rows(x, "x")
+    ldr = 0 if residual is None else _rows(residual, "residual", x)
+    y = _new_rows(x) if out is None else out
+    ldy = _rows(y, "out", x)
+    _check(lib().fa4_dropout_fwd(_ptr(x), ldx, _ptr(residual), ldr, x.shape[0], x.shape[1],
+                                 DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF, _step(step, x),
+                                 _ptr(y), ldy, _stream(x.device)), "fa4_dropout_fwd")
+    return y
+
+
+@_on_tensor_device
+def dropout_bwd(dy: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """dx of dropout_fwd under the same p, seed and step (the residual's
+    gradient is dy itself).  out may be dy."""
+    lddy = _rows(dy, "dy")
+    dx = _new_rows(dy) if out is None else out
+    lddx = _rows(dx, "out", dy)
+    _check(lib().fa4_dropout_bwd(_ptr(dy), lddy, dy.shape[0], dy.shape[1], DTYPE[dy.dtype], p,
+                                 seed & 0xFFFFFFFFFFFFFFFF, _step(step, dy), _ptr(dx), lddx,
+                                 _stream(dy.device)), "fa4_dropout_bwd")
+    return dx
+
+
+@_on_tensor_device
+def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
+                               bias: torch.Tensor | None, p: float, seed: int,
+                               step: torch.Tensor | None = None, eps: float = 1e-5,
+                               center: bool = True, out: torch.Tensor | None = None,
+                               s: torch.Tensor | None = None
+                               ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor | None, torch.Tensor]:
+    """(y, s, mean, rstd) in one pass over the data: s = residual + dropout(x)
+    as dropout_fwd gives it, y = the layer norm of the stored s.  s may be
+    residual and out may be x."""
+    ldx, ldr = _rows(x, "x"), _rows(residual, "residual", x)
+    wd = _weights(weight, bias, x)
+    y = _new_rows(x) if out is None else out
+    s = _new_rows(x) if s is None else s
+    ldy, lds = _rows(y, "out", x), _rows(s, "s", x)
+    T, N = x.shape
+    mean = torch.empty(T, dtype=torch.float32, device=x.device) if center else None
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check(lib().fa4_dropout_add_layernorm_fwd(
+        _ptr(x), ldx, _ptr(residual), ldr, T, N, DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF,
+        _step(step, x), _ptr(weight), _ptr(bias), wd, eps, 1 if center else 0, _ptr(s), lds, _ptr(y),
+        ldy, _ptr(mean), _ptr(rstd), _stream(x.device)), "fa4_dropout_add_layernorm_fwd")
+    return y, s, mean, rstd
+
+
+@_on_tensor_device
+def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: torch.Tensor,
+                               weight: torch.Tensor, mean: torch.Tensor | None, rstd: torch.Tensor,
+                               p: float, seed: int, step: torch.Tensor | None = None,
+                               center: bool = True, bias_grad: bool = True,
+                               dx: torch.Tensor | None = None, dres: torch.Tensor | None = None,
+                               dweight: torch.Tensor | None = None,
+                               dbias: torch.Tensor | None = None, ws: torch.Tensor | None = None
+                               ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor | None]:
+    """(dx, dres, dweight, dbias) of dropout_add_layer_norm_fwd: dres, the
+    gradient of residual, is the norm's gradient of s plus ds (the gradient
+    that reaches s by another way, or None); dx = dropout of that sum under
+    the same p, seed and step."""
+    lds, lddy = _rows(s, "s"), _rows(dy, "dy", s)
+    ldds = 0 if ds is None else _rows(ds, "ds", s)
+    wd = _weights(weight, None, s)
+    _stats(mean, rstd, center, s)
+    dx = _new_rows(s) if dx is None else dx
+    dres = _new_rows(s) if dres is None else dres
+    lddx, lddr = _rows(dx, "dx", s), _rows(dres, "dres", s)
+    dweight, dbias = _grads(dweight, dbias, bias_grad, s)
+    ws = _norm_ws(ws, s)
+    T, N = s.shape
+    _check(lib().fa4_dropout_add_layernorm_bwd(
+        _ptr(dy), lddy, _ptr(ds), ldds, _ptr(s), lds, T, N, DTYPE[s.dtype], p,
+        seed & 0xFFFFFFFFFFFFFFFF, _step(step, s), _ptr(weight), wd, 1 if center else 0,
+        _ptr(mean) if center else None, _ptr(rstd), _ptr(dx), lddx, _ptr(dres), lddr, _ptr(dweight),
+        _ptr(dbias), _ptr(ws), ws.numel(), _stream(s.device)), "fa4_dropout_add_layernorm_bwd")
+    return dx, dres, dweight, dbias
+
+
+@_on_tensor_device
+def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """dz[T, 2F] of the SwiGLU producer (swiglu_quantize) from the gradient
+    dh[T, F] of h: the dY that linear_bwd of the gate+up linear takes.  out
+    may be z."""
+    ldz, lddh = _as_bf16_2d(z, "z"), _as_bf16_2d(dh, "dh")
+    T, F2 = z.shape
+    if F2 % 2 or dh.shape != (T, F2 // 2) or dh.device != z.device:
+        raise ValueError(f"z must hold gate and up halves and dh must be [{T}, {F2 // 2}] on {z.device}")
+    if out is None:
+        out = torch.empty((T, F2), dtype=torch.bfloat16, device=z.device)
+    else:
+        _check_out(out, (T, F2), (torch.bfloat16,), z.device, "out", row_stride=True)
+    _check(lib().fa4_swiglu_bwd(_ptr(z), ldz, _ptr(dh), lddh, T, F2 // 2, _ptr(out), out.stride(0),
+                                _stream(z.device)), "fa4_swiglu_bwd")
+    return out

@@ -2,6 +2,7 @@
 // host, workspace carving, and kernel launches.  No device memory is
 // allocated here and nothing synchronizes except fa4_check_device_status.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -204,6 +205,51 @@ fa4_status check_gemm(const fa4_qtensor &A, const fa4_qtensor &B, int64_t M, int
   if (!ws || ws_bytes < kHdr) return FA4_ERR_WORKSPACE;
   if (!aligned16(ws)) return FA4_ERR_ALIGN;
   return FA4_OK;
+}
+
+// ---- row-wise training operators
+inline bool dtype_ok(int d) { return d == FA4_BF16 || d == FA4_FP32 || d == FA4_FP16; }
+inline bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline size_t dtype_size(int d) { return d == FA4_FP32 ? 4 : 2; }
+// A required matrix of the call.
+fa4_status check_rows(const void *p, int64_t ld, int64_t N, int dtype) {
+  if (!p) return FA4_ERR_INVALID_ARG;
+  if (ld < N) return FA4_ERR_SHAPE;
+  return aligned_to(p, dtype_size(dtype)) ? FA4_OK : FA4_ERR_ALIGN;
+}
+// The matrices' sizes; rows and column blocks are 32-bit generator counters.
+bool rows_shape_ok(int64_t T, int64_t N) {
+  return T > 0 && N > 0 && T < (int64_t(1) << 32) && N < (int64_t(1) << 31);
+}
+fa4_status check_weights(const void *w, const void *b, int w_dtype, int dtype) {
+  if (!w || !dtype_ok(w_dtype)) return FA4_ERR_INVALID_ARG;
+  if (w_dtype != dtype && w_dtype != FA4_FP32) return FA4_ERR_UNSUPPORTED;
+  const size_t n = dtype_size(w_dtype);
+  return aligned_to(w, n) && aligned_to(b, n) ? FA4_OK : FA4_ERR_ALIGN;
+}
+fa4_status check_stats(const float *mean, const float *rstd, int center) {
+  if ((center != 0 && center != 1) || !rstd || (center && !mean)) return FA4_ERR_INVALID_ARG;
+  return aligned4(rstd) && aligned4(mean) ? FA4_OK : FA4_ERR_ALIGN;
+}
+fa4_status make_drop(double p, uint64_t seed, const uint64_t *step, fa4::DropArgs *d) {
+  if (!(p >= 0.0 && p < 1.0)) return FA4_ERR_INVALID_ARG;  // NaN too
+  if (!aligned_to(step, 8)) return FA4_ERR_ALIGN;
+  const double t = nearbyint(p * 65536.0);
+  d->seed = seed;
+  d->step = step;
+  d->threshold = t > 65535.0 ? 65535u : (uint32_t)t;
+  d->scale = (float)(65536.0 / (65536.0 - d->threshold));
+  return FA4_OK;
+}
+size_t norm_ws(int64_t T, int64_t N) {
+  return kHdr + align256(sizeof(float) * 2 * (size_t)N * (size_t)fa4::norm_partials_count(T, N));
+}
+fa4_status check_norm_bwd_out(int64_t T, int64_t N, const float *dw, const float *db, const void *ws,
+                              size_t ws_bytes) {
+  if (!dw) return FA4_ERR_INVALID_ARG;
+  if (!aligned4(dw) || !aligned4(db)) return FA4_ERR_ALIGN;
+  if (!ws || ws_bytes < norm_ws(T, N)) return FA4_ERR_WORKSPACE;
+  return aligned16(ws) ? FA4_OK : FA4_ERR_ALIGN;
 }
 
 }  // namespace
@@ -482,6 +528,206 @@ fa4_status fa4_gemm_blockscaled_mxout(fa4_qtensor A, fa4_qtensor B, int64_t M, i
     return s;
   return do_gemm(A, B, M, N, K, fmt, alpha, D, D ? ldd : N, FA4_OUT_BF16,
                  static_cast<uint8_t *>(workspace), S(stream), -1, kDefaultTimeoutNs, &Dq);
+}
+
+fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int64_t N, fa4_dtype dtype,
+                             const void *weight, const void *bias, fa4_dtype w_dtype, float eps,
+                             int center, void *y, int64_t ldy, float *mean, float *rstd,
+                             void *stream) {
+  if (!dtype_ok(dtype) || !(eps >= 0.0f) || isinf(eps)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4_status s = check_rows(x, ldx, N, dtype);
+  if (s != FA4_OK || (s = check_rows(y, ldy, N, dtype)) != FA4_OK ||
+      (s = check_weights(weight, bias, w_dtype, dtype)) != FA4_OK ||
+      (s = check_stats(mean, rstd, center)) != FA4_OK)
+    return s;
+  fa4::NormFwdArgs a = {};
+  a.fused = false;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.x = x;
+  a.ldx = ldx;
+  a.w = weight;
+  a.b = bias;
+  a.w_f32 = w_dtype == FA4_FP32;
+  a.center = center;
+  a.eps = eps;
+  a.y = y;
+  a.ldy = ldy;
+  a.mean = mean;
+  a.rstd = rstd;
+  return cuda_status(fa4::launch_norm_fwd(a, S(stream)));
+}
+
+fa4_status fa4_layernorm_ws_bytes(int64_t T, int64_t N, size_t *workspace_bytes) {
+  if (!workspace_bytes) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  *workspace_bytes = norm_ws(T, N);
+  return FA4_OK;
+}
+
+fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                             const void *dres, int64_t lddres, int64_t T, int64_t N, fa4_dtype dtype,
+                             const void *weight, fa4_dtype w_dtype, int center, const float *mean,
+                             const float *rstd, void *dx, int64_t lddx, float *dweight, float *dbias,
+                             void *workspace, size_t workspace_bytes, void *stream) {
+  if (!dtype_ok(dtype)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4_status s = check_rows(dy, lddy, N, dtype);
+  if (s != FA4_OK || (s = check_rows(x, ldx, N, dtype)) != FA4_OK ||
+      (dres && (s = check_rows(dres, lddres, N, dtype)) != FA4_OK) ||
+      (s = check_rows(dx, lddx, N, dtype)) != FA4_OK ||
+      (s = check_weights(weight, nullptr, w_dtype, dtype)) != FA4_OK ||
+      (s = check_stats(mean, rstd, center)) != FA4_OK ||
+      (s = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
+    return s;
+  fa4::NormBwdArgs a = {};
+  a.fused = false;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.ds = dres;
+  a.ldds = lddres;
+  a.w = weight;
+  a.w_f32 = w_dtype == FA4_FP32;
+  a.center = center;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dweight;
+  a.db = dbias;
+  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
+  return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
+}
+
+fa4_status fa4_dropout_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldres, int64_t T,
+                           int64_t N, fa4_dtype dtype, double p, uint64_t seed, const uint64_t *step,
+                           void *y, int64_t ldy, void *stream) {
+  if (!dtype_ok(dtype)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4::DropoutArgs a = {};
+  fa4_status s = check_rows(x, ldx, N, dtype);
+  if (s != FA4_OK || (residual && (s = check_rows(residual, ldres, N, dtype)) != FA4_OK) ||
+      (s = check_rows(y, ldy, N, dtype)) != FA4_OK ||
+      (s = make_drop(p, seed, step, &a.drop)) != FA4_OK)
+    return s;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.x = x;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldres = ldres;
+  a.y = y;
+  a.ldy = ldy;
+  return cuda_status(fa4::launch_dropout(a, S(stream)));
+}
+
+fa4_status fa4_dropout_bwd(const void *dy, int64_t lddy, int64_t T, int64_t N, fa4_dtype dtype,
+                           double p, uint64_t seed, const uint64_t *step, void *dx, int64_t lddx,
+                           void *stream) {
+  return fa4_dropout_fwd(dy, lddy, nullptr, 0, T, N, dtype, p, seed, step, dx, lddx, stream);
+}
+
+fa4_status fa4_dropout_add_layernorm_fwd(const void *x, int64_t ldx, const void *residual,
+                                         int64_t ldres, int64_t T, int64_t N, fa4_dtype dtype,
+                                         double p, uint64_t seed, const uint64_t *step,
+                                         const void *weight, const void *bias, fa4_dtype w_dtype,
+                                         float eps, int center, void *s, int64_t lds, void *y,
+                                         int64_t ldy, float *mean, float *rstd, void *stream) {
+  if (!dtype_ok(dtype) || !(eps >= 0.0f) || isinf(eps)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4::NormFwdArgs a = {};
+  fa4_status e = check_rows(x, ldx, N, dtype);
+  if (e != FA4_OK || (e = check_rows(residual, ldres, N, dtype)) != FA4_OK ||
+      (e = check_rows(s, lds, N, dtype)) != FA4_OK || (e = check_rows(y, ldy, N, dtype)) != FA4_OK ||
+      (e = check_weights(weight, bias, w_dtype, dtype)) != FA4_OK ||
+      (e = check_stats(mean, rstd, center)) != FA4_OK ||
+      (e = make_drop(p, seed, step, &a.drop)) != FA4_OK)
+    return e;
+  a.fused = true;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.x = x;
+  a.ldx = ldx;
+  a.res = residual;
+  a.ldres = ldres;
+  a.w = weight;
+  a.b = bias;
+  a.w_f32 = w_dtype == FA4_FP32;
+  a.center = center;
+  a.eps = eps;
+  a.s = s;
+  a.lds = lds;
+  a.y = y;
+  a.ldy = ldy;
+  a.mean = mean;
+  a.rstd = rstd;
+  return cuda_status(fa4::launch_norm_fwd(a, S(stream)));
+}
+
+fa4_status fa4_dropout_add_layernorm_bwd(const void *dy, int64_t lddy, const void *ds, int64_t ldds,
+                                         const void *s, int64_t lds, int64_t T, int64_t N,
+                                         fa4_dtype dtype, double p, uint64_t seed,
+                                         const uint64_t *step, const void *weight, fa4_dtype w_dtype,
+                                         int center, const float *mean, const float *rstd, void *dx,
+                                         int64_t lddx, void *dres, int64_t lddres, float *dweight,
+                                         float *dbias, void *workspace, size_t workspace_bytes,
+                                         void *stream) {
+  if (!dtype_ok(dtype)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4::NormBwdArgs a = {};
+  fa4_status e = check_rows(dy, lddy, N, dtype);
+  if (e != FA4_OK || (ds && (e = check_rows(ds, ldds, N, dtype)) != FA4_OK) ||
+      (e = check_rows(s, lds, N, dtype)) != FA4_OK || (e = check_rows(dx, lddx, N, dtype)) != FA4_OK ||
+      (e = check_rows(dres, lddres, N, dtype)) != FA4_OK ||
+      (e = check_weights(weight, nullptr, w_dtype, dtype)) != FA4_OK ||
+      (e = check_stats(mean, rstd, center)) != FA4_OK ||
+      (e = make_drop(p, seed, step, &a.drop)) != FA4_OK ||
+      (e = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
+    return e;
+  a.fused = true;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = s;
+  a.ldx = lds;
+  a.ds = ds;
+  a.ldds = ldds;
+  a.w = weight;
+  a.w_f32 = w_dtype == FA4_FP32;
+  a.center = center;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dres = dres;
+  a.lddres = lddres;
+  a.dw = dweight;
+  a.db = dbias;
+  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
+  return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
+}
+
+fa4_status fa4_swiglu_bwd(const void *z, int64_t ldz, const void *dh, int64_t lddh, int64_t T,
+                          int64_t F, void *dz, int64_t lddz, void *stream) {
+  if (!z || !dh || !dz) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, F) || F % 8 || ldz < 2 * F || ldz % 8 || lddz < 2 * F || lddz % 8 || lddh < F ||
+      lddh % 8)
+    return FA4_ERR_SHAPE;
+  if (!aligned16(z) || !aligned16(dh) || !aligned16(dz)) return FA4_ERR_ALIGN;
+  const fa4::SwigluBwdArgs a = {static_cast<const uint16_t *>(z), static_cast<const uint16_t *>(dh),
+                                static_cast<uint16_t *>(dz), T, F, ldz, lddh, lddz};
+  return cuda_status(fa4::launch_swiglu_bwd(a, S(stream)));
 }
 
 fa4_status fa4_workspace_init(void *workspace, size_t workspace_bytes, void *stream) {

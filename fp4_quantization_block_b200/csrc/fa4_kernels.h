@@ -88,4 +88,66 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm_blockscaled(const GemmArgs &a, cudaStream_t st);
 
+// ---- row-wise training operators (norm.cu, dropout.cu, swiglu_bwd.cu)
+enum : int { kBF16 = 0, kFP32 = 1, kFP16 = 2 };  // fa4_dtype
+struct DropArgs {
+  uint64_t seed = 0;
+  const uint64_t *step = nullptr;  // device scalar added to seed, or null
+  uint32_t threshold = 0;          // drop probability x 65536
+  float scale = 1.0f;              // 65536 / (65536 - threshold)
+};
+// Layer norm of x[T, N], or (fused) of s = res + dropout(x), which is stored.
+struct NormFwdArgs {
+  bool fused;
+  int dtype;
+  int64_t T, N;
+  const void *x, *res;
+  int64_t ldx, ldres;
+  const void *w, *b;  // b may be null
+  int w_f32, center;
+  float eps;
+  void *y, *s;
+  int64_t ldy, lds;
+  float *mean, *rstd;  // mean may be null without centring
+  DropArgs drop;
+};
+cudaError_t launch_norm_fwd(const NormFwdArgs &a, cudaStream_t st);
+// Its backward pass: dx (+ ds), dw, db (may be null).  Fused: dres takes that
+// dx and dx = dropout(dres).
+struct NormBwdArgs {
+  bool fused;
+  int dtype;
+  int64_t T, N;
+  const void *dy, *x, *ds;  // ds may be null
+  int64_t lddy, ldx, ldds;
+  const void *w;
+  int w_f32, center;
+  const float *mean, *rstd;
+  void *dx, *dres;
+  int64_t lddx, lddres;
+  float *dw, *db;
+  float *partials;  // norm_partials_count(T, N) * 2 * N
+  DropArgs drop;
+};
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t st);
+constexpr int kMaxNormPartials = 1184;
+int norm_partials_count(int64_t T, int64_t N);
+// y = [res +] dropout(x)
+struct DropoutArgs {
+  int dtype;
+  int64_t T, N;
+  const void *x, *res;  // res may be null
+  void *y;
+  int64_t ldx, ldres, ldy;
+  DropArgs drop;
+};
+cudaError_t launch_dropout(const DropoutArgs &a, cudaStream_t st);
+// dz of h = silu(gate) * up, z[T, 2F] = gate | up
+struct SwigluBwdArgs {
+  const uint16_t *z, *dh;
+  uint16_t *dz;
+  int64_t T, F, ldz, lddh, lddz;
+};
+cudaError_t launch_swiglu_bwd(const SwigluBwdArgs &a, cudaStream_t st);
+
 }  // namespace fa4

@@ -331,6 +331,111 @@ FA4_API fa4_status fa4_quantize_nvfp4_global_noalloc(const void *x, int64_t rows
                                                      int64_t ld, fa4_round rnd, fa4_orient orient,
                                                      uint64_t seed, fa4_qtensor out, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Training operators between the linears: layer norm, dropout, the two fused
+ * with the residual addition, and the SwiGLU producer's backward pass.  The
+ * pages report pretraining of Llama-3-family blocks ("Format-Aware Fusion:
+ * The Engineering Practice That Doubles FP4 Pretraining Throughput", section
+ * "Empirical Results") and give no numerics for these steps; they are defined
+ * here.
+ *
+ * Matrices are row-major [T, N] with leading dimensions in ELEMENTS, at least
+ * the row length; 1 <= T < 2^32, 1 <= N < 2^31.  Unlike the quantizers' any N,
+ * any leading dimension and any pointer aligned to its element are taken;
+ * rows that start on 16-byte boundaries with N a multiple of 8 are the fast
+ * ones.  `dtype` is the type of every matrix of the call; weight and bias are
+ * of w_dtype, which is `dtype` or FA4_FP32.  Arithmetic, statistics and sums
+ * are binary32; a value is rounded once, where it is stored.  Non-finite
+ * values are allowed and stay within the rows (and, in the gradients of
+ * weight and bias, the columns) that depend on them. */
+typedef enum { FA4_BF16 = 0, FA4_FP32 = 1, FA4_FP16 = 2 } fa4_dtype;
+
+/* Layer norm.  For each row x of N values:
+ *   mean = sum(x) / N (with center = 0: the RMS form, 0 and not written),
+ *   rstd = (sum((x - mean)^2) / N + eps)^-1/2,
+ *   y = (x - mean) * rstd * weight + bias.
+ * mean[T] and rstd[T] (binary32) are kept for the backward pass; mean may be
+ * NULL when center is 0.  bias may be NULL.  eps >= 0 (a constant row with
+ * eps = 0 gives non-finite values, as the formula does).  y may be x itself
+ * (same leading dimension); otherwise outputs overlap no input.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (w_dtype), CUDA. */
+FA4_API fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int64_t N,
+                                     fa4_dtype dtype, const void *weight, const void *bias,
+                                     fa4_dtype w_dtype, float eps, int center, void *y,
+                                     int64_t ldy, float *mean, float *rstd, void *stream);
+
+/* Its backward pass.  With xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum(g) / N - xh * sum(g xh) / N) + dres
+ * (without sum(g) / N when center is 0; dres, the gradient that reaches x by
+ * another way, e.g. the residual stream, may be NULL),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy (binary32
+ * [N]; dbias may be NULL).  The sums over the rows are taken in a fixed order:
+ * a call repeats bit for bit.  dx may be dy, x or dres itself (same leading
+ * dimension).  Workspace: fa4_layernorm_ws_bytes (nothing in it has to be
+ * zero); calls that may run at the same time need one each.
+ * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (w_dtype), WORKSPACE, CUDA. */
+FA4_API fa4_status fa4_layernorm_ws_bytes(int64_t T, int64_t N, size_t *workspace_bytes);
+FA4_API fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                     const void *dres, int64_t lddres, int64_t T, int64_t N,
+                                     fa4_dtype dtype, const void *weight, fa4_dtype w_dtype,
+                                     int center, const float *mean, const float *rstd, void *dx,
+                                     int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/* Dropout of x[T, N] with a mask that is a function of (key, row, column) and
+ * is never stored: element (r, c) has 16 random bits u, half c & 1 of word
+ * (c >> 1) & 3 of Philox4x32-7 on the counter (c >> 3, r, 0, 0x44524F50)
+ * under the 64-bit key seed + *step, and is dropped iff u < t, t = min(
+ * rint(65536 p), 65535).  y = x * 65536 / (65536 - t) where kept (the exact
+ * reciprocal of the probability of being kept), 0 where dropped, whatever the
+ * dropped value was; plus residual when it is not NULL.  0 <= p < 1.  step is
+ * a device pointer to one 64-bit integer or NULL (0): a captured graph draws
+ * a new mask at each replay when the caller advances it.  The counters never
+ * meet the stochastic rounding's, under any key.  y may be x or residual
+ * itself (same leading dimension).
+ * fa4_dropout_bwd: dx from dy, the same p, seed and *step (the gradient of
+ * the residual is dy itself).
+ * Errors: INVALID_ARG, SHAPE, ALIGN, CUDA. */
+FA4_API fa4_status fa4_dropout_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldres,
+                                   int64_t T, int64_t N, fa4_dtype dtype, double p, uint64_t seed,
+                                   const uint64_t *step, void *y, int64_t ldy, void *stream);
+FA4_API fa4_status fa4_dropout_bwd(const void *dy, int64_t lddy, int64_t T, int64_t N,
+                                   fa4_dtype dtype, double p, uint64_t seed, const uint64_t *step,
+                                   void *dx, int64_t lddx, void *stream);
+
+/* Dropout, residual and layer norm in one pass over the data:
+ *   s = residual + dropout(x) (stored),  y = layer norm of the stored s.
+ * s equals fa4_dropout_fwd's y.  s may be residual itself and y may be x
+ * itself (same leading dimensions).
+ * Backward: dy is the gradient of y and ds (may be NULL) the one that reaches
+ * s by another way; dres = layer norm's dx + ds, the gradient of residual;
+ * dx = dropout of that same sum, before dres is rounded.  dx and dres may be
+ * dy, s or ds themselves (two different ones, same leading dimensions).
+ * Workspace: fa4_layernorm_ws_bytes.
+ * Errors: as fa4_layernorm_fwd / _bwd and fa4_dropout_fwd. */
+FA4_API fa4_status fa4_dropout_add_layernorm_fwd(
+    const void *x, int64_t ldx, const void *residual, int64_t ldres, int64_t T, int64_t N,
+    fa4_dtype dtype, double p, uint64_t seed, const uint64_t *step, const void *weight,
+    const void *bias, fa4_dtype w_dtype, float eps, int center, void *s, int64_t lds, void *y,
+    int64_t ldy, float *mean, float *rstd, void *stream);
+FA4_API fa4_status fa4_dropout_add_layernorm_bwd(
+    const void *dy, int64_t lddy, const void *ds, int64_t ldds, const void *s, int64_t lds,
+    int64_t T, int64_t N, fa4_dtype dtype, double p, uint64_t seed, const uint64_t *step,
+    const void *weight, fa4_dtype w_dtype, int center, const float *mean, const float *rstd,
+    void *dx, int64_t lddx, void *dres, int64_t lddres, float *dweight, float *dbias,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of the SwiGLU producer (fa4_swiglu_quantize): z[T, 2F] as
+ * there, dh[T, F] the bf16 gradient of h.  With sg = 1 / (1 + exp(-gate)):
+ *   dz[:, 0:F]  = dh * up * sg * (1 + gate * (1 - sg)),
+ *   dz[:, F:2F] = dh * gate * sg,
+ * binary32, each rounded once to bf16: the dY that fa4_linear_bwd of the
+ * gate+up linear takes.  F and the leading dimensions multiples of 8, ldz and
+ * lddz >= 2F, lddh >= F; pointers 16-byte aligned.  dz may be z itself (same
+ * leading dimension).  Errors: INVALID_ARG, SHAPE, ALIGN, CUDA. */
+FA4_API fa4_status fa4_swiglu_bwd(const void *z, int64_t ldz, const void *dh, int64_t lddh,
+                                  int64_t T, int64_t F, void *dz, int64_t lddz, void *stream);
+
 /* Zero the workspace header (stream-ordered memset of FA4_WS_HEADER_BYTES). */
 FA4_API fa4_status fa4_workspace_init(void *workspace, size_t workspace_bytes, void *stream);
 

@@ -1,0 +1,295 @@
+"""Layer norm and its fusion with dropout and the residual addition, forward
+and backward, against 64-bit plain forms (rows_ref.py) within bounds derived
+there: every type, row lengths that end inside a chunk, a warp or a CTA's
+columns, leading dimensions and offsets that are not aligned, one row and many,
+extreme rows, in-place outputs, other streams, captured graphs."""
+import pytest
+import torch
+
+import fp4_quantization_block_b200 as fa
+import rows_ref as R
+from gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+EPS = 1e-5
+SEED = 0xFEDCBA9876543210
+
+
+def held(x, dtype, pad=0, offset=0, fill=None):
+    """x on the GPU in `dtype`, its rows x.shape[1] + pad apart, starting
+    `offset` elements into a 16-byte aligned buffer."""
+    T, N = x.shape
+    buf = torch.full((T * (N + pad) + offset + 64,), 0.0 if fill is None else fill, dtype=dtype,
+                     device="cuda")
+    v = buf[offset:offset + T * (N + pad)].view(T, N + pad)[:, :N]
+    v.copy_(x)
+    return v
+
+
+def inputs(T, N, dtype, seed, wtype=None, bias=True, pad=0, offset=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, N, generator=g) + 0.5 * torch.randn(1, N, generator=g) + 0.3
+    x[:, :: 97] *= 20.0
+    r = torch.randn(T, N, generator=g)
+    dy = torch.randn(T, N, generator=g) * torch.randn(T, 1, generator=g).exp() * 1e-2
+    ds = torch.randn(T, N, generator=g) * 1e-2
+    w = (1 + 0.3 * torch.randn(N, generator=g)).to(wtype or dtype)
+    b = (0.2 * torch.randn(N, generator=g)).to(wtype or dtype) if bias else None
+    mats = [held(m, dtype, pad, offset) for m in (x, r, dy, ds)]
+    return mats, w.cuda(), b.cuda() if bias else None
+
+
+def cpu(*ts):
+    return [None if t is None else t.cpu() for t in ts]
+
+
+def check_fwd(x, w, b, center, y, mean, rstd):
+    xc, wc, bc = cpu(x, w, b)
+    (ye, me, re), (by, bm, br) = R.norm_fwd(xc, wc, bc, EPS, center)
+    R.check("y", y, ye, by, y.dtype)
+    R.check("rstd", rstd, re, br)
+    if center:
+        R.check("mean", mean, me, bm)
+    else:
+        assert mean is None
+
+
+def check_bwd(dy, x, w, mean, rstd, center, dres, dx, dw, db):
+    c = cpu(dy, x, w, mean, rstd, dres)
+    (dxe, dwe, dbe), (bx, bw, bb) = R.norm_bwd(c[0], c[1], c[2], c[3], c[4], center, c[5])
+    R.check("dx", dx, dxe, bx, dx.dtype)
+    R.check("dweight", dw, dwe, bw)
+    if db is not None:
+        R.check("dbias", db, dbe, bb)
+
+
+# row lengths: one value, less than a chunk, chunks that end inside a warp,
+# the borders of each layout, odd ones, and rows too long for the chip's ring
+SHAPES = [(1, 1), (3, 5), (5, 8), (37, 64), (64, 200), (9, 256), (130, 264), (33, 512), (17, 520),
+          (40, 1000), (1, 1024), (300, 1032), (67, 2048), (1, 4096), (150, 4096), (21, 4099),
+          (700, 768), (5, 8192), (12, 8200), (7, 14336), (4, 16384), (3, 16392), (2, 28672),
+          (2, 40001)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("T,N", SHAPES, ids=[f"{t}x{n}" for t, n in SHAPES])
+def test_norm_fwd_and_bwd(T, N, dtype):
+    need_gpu()
+    (x, _, dy, ds), w, b = inputs(T, N, dtype, seed=T * 100003 + N)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    check_fwd(x, w, b, True, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd)
+    check_bwd(dy, x, w, mean, rstd, True, None, dx, dw, db)
+    dx, dw2, db2 = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    check_bwd(dy, x, w, mean, rstd, True, ds, dx, dw2, db2)
+    assert torch.equal(dw, dw2) and torch.equal(db, db2)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("T,N", [(19, 72), (33, 1000), (50, 4096), (6, 14336), (2, 20000)],
+                         ids=lambda v: str(v))
+def test_rms_form_and_binary32_weights(T, N, dtype):
+    need_gpu()
+    (x, _, dy, ds), w, _ = inputs(T, N, dtype, seed=N, wtype=torch.float32, bias=False)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, None, EPS, center=False)
+    check_fwd(x, w, None, False, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, None, rstd, center=False, bias_grad=False, dres=ds)
+    assert db is None
+    check_bwd(dy, x, w, None, rstd, False, ds, dx, dw, None)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1), (5, 3), (2, 2)],
+                         ids=lambda v: str(v))
+@pytest.mark.parametrize("N", [40, 771, 4096, 4098, 18433])
+def test_leading_dimensions_and_offsets(N, pad, offset, dtype):
+    """Strided and offset matrices; what lies between the rows stays as it was."""
+    need_gpu()
+    T = 5
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=N + pad, pad=pad, offset=offset)
+    outs = [held(torch.zeros(T, N), dtype, pad, offset, fill=7.0) for _ in range(4)]
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS, out=outs[0])
+    check_fwd(x, w, b, True, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds, dx=outs[1])
+    check_bwd(dy, x, w, mean, rstd, True, ds, dx, dw, db)
+    y2, s, m2, r2 = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.25, SEED, out=outs[2], s=outs[3])
+    assert torch.equal(s, fa.dropout_fwd(x, 0.25, SEED, residual=r))
+    check_fwd(s, w, b, True, y2, m2, r2)
+    for o in outs:
+        whole = torch.as_strided(o, (T * (N + pad),), (1,), o.storage_offset())
+        between = whole.view(T, N + pad)[:, N:]
+        assert torch.all(between == 7.0)
+        base = torch.as_strided(o, (offset,), (1,), 0)
+        end = torch.as_strided(o, (64,), (1,), o.storage_offset() + T * (N + pad))
+        assert torch.all(base == 7.0) and torch.all(end == 7.0)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("center", [True, False], ids=["layer", "rms"])
+@pytest.mark.parametrize("T,N,p", [(1, 1, 0.5), (3, 13, 0.1), (40, 512, 0.1), (17, 1001, 0.0),
+                                   (21, 4096, 0.1), (3, 14336, 0.5), (2, 17000, 0.25)],
+                         ids=lambda v: str(v))
+def test_fused_with_dropout_and_residual(T, N, p, center, dtype):
+    need_gpu()
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=T + N)
+    step = torch.tensor([41], dtype=torch.int64, device="cuda")
+    y, s, mean, rstd = fa.dropout_add_layer_norm_fwd(x, r, w, b, p, SEED, step=step, center=center)
+    mask, scale = R.kept(T, N, p, SEED, 41)
+    xc, rc = cpu(x, r)
+    de, db_ = R.drop(xc, mask, scale)
+    se = rc.double() + de
+    R.check("s", s, se, db_ + R.U * se.abs(), dtype)
+    assert torch.equal(s, fa.dropout_fwd(x, p, SEED, step=step, residual=r))
+    check_fwd(s, w, b, center, y, mean, rstd)
+
+    for d in (ds, None):
+        dx, dres, dw, db = fa.dropout_add_layer_norm_bwd(dy, d, s, w, mean, rstd, p, SEED, step=step,
+                                                         center=center)
+        check_bwd(dy, s, w, mean, rstd, center, d, dres, dw, db)
+        c = cpu(dy, s, w, mean, rstd, d)
+        (full, _, _), (bound, _, _) = R.norm_bwd(*c[:5], center, c[5])
+        want, b3 = R.drop(full, mask, scale)
+        R.check("dx", dx, want, torch.where(mask, bound * scale, 0.0) + b3, dtype)
+        assert torch.all(dx.cpu()[~mask] == 0)
+
+
+def test_against_differences():
+    """dx, dweight and dbias against central differences of the 64-bit forward
+    pass along random directions (binary32 inputs; the differences' own error
+    at h = 1e-4 is below 1e-7 of the sums compared)."""
+    need_gpu()
+    T, N = 6, 96
+    (x, _, dy, _), w, b = inputs(T, N, torch.float32, seed=5)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd)
+    xc, wc, bc, dyc = (t.double().cpu() for t in (x, w, b, dy))
+    g = torch.Generator().manual_seed(1)
+
+    def loss(xv, wv, bv):
+        d = xv - xv.mean(1, keepdim=True)
+        return float(((d * (d.square().mean(1, keepdim=True) + EPS).rsqrt() * wv + bv) * dyc).sum())
+
+    h = 1e-4
+    for k in range(8):
+        vx, vw, vb = (torch.randn(t.shape, generator=g, dtype=torch.float64) for t in (xc, wc, bc))
+        for v, grad, f in ((vx, dx, lambda e: loss(xc + e * vx, wc, bc)),
+                           (vw, dw, lambda e: loss(xc, wc + e * vw, bc)),
+                           (vb, db, lambda e: loss(xc, wc, bc + e * vb))):
+            want = (f(h) - f(-h)) / (2 * h)
+            terms = grad.double().cpu() * v
+            # 64 u on each term covers the gradients' bounds at N = 96
+            tol = 64 * R.U * float(terms.abs().sum()) + 1e-6 * float(terms.abs().sum())
+            assert abs(float(terms.sum()) - want) <= tol, (k, float(terms.sum()), want)
+
+
+@pytest.mark.parametrize("N", [512, 4096, 17000])
+def test_extreme_rows(N):
+    """A constant row, a row of zeros, a huge mean, tiny values; infinities and
+    NaN stay in their rows."""
+    need_gpu()
+    (x, _, dy, _), w, b = inputs(8, N, torch.float32, seed=3)
+    x[0] = 3.0
+    x[1] = 0.0
+    x[2] += 1.0e4
+    x[3] *= 1e-30
+    ref = x.clone()
+    x[5, N // 2] = float("inf")
+    x[6, 1] = float("nan")
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    fine = [0, 1, 2, 3, 4, 7]
+    check_fwd(ref[fine], w, b, True, y[fine], mean[fine], rstd[fine])
+    assert torch.isnan(y[5, N // 2]) and torch.isnan(y[6]).all()
+    dx, _, _ = fa.layer_norm_bwd(dy, x, w, mean, rstd)
+    dx2, _, _ = fa.layer_norm_bwd(dy[fine].contiguous(), ref[fine].contiguous(), w,
+                                  mean[fine].contiguous(), rstd[fine].contiguous())
+    assert torch.equal(dx[fine], dx2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N", [96, 4096, 4099, 17000])
+def test_in_place(N, dtype):
+    need_gpu()
+    T = 9
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=N)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    xi = x.clone()
+    fa.layer_norm_fwd(xi, w, b, EPS, out=xi)
+    assert torch.equal(xi, y)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    for k in range(3):
+        a = [dy.clone(), x.clone(), ds.clone()]
+        _, dw2, db2 = fa.layer_norm_bwd(a[0], a[1], w, mean, rstd, dres=a[2], dx=a[k])
+        assert torch.equal(a[k], dx) and torch.equal(dw, dw2) and torch.equal(db, db2)
+    y, s, mean, rstd = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+    xi, ri = x.clone(), r.clone()
+    fa.dropout_add_layer_norm_fwd(xi, ri, w, b, 0.1, SEED, out=xi, s=ri)
+    assert torch.equal(xi, y) and torch.equal(ri, s)
+    want = fa.dropout_add_layer_norm_bwd(dy, ds, s, w, mean, rstd, 0.1, SEED)
+    di, si = dy.clone(), ds.clone()
+    got = fa.dropout_add_layer_norm_bwd(di, si, s, w, mean, rstd, 0.1, SEED, dx=di, dres=si)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_repeats_bit_for_bit_with_a_dirty_workspace():
+    need_gpu()
+    T, N = 1000, 4096
+    (x, _, dy, ds), w, b = inputs(T, N, torch.bfloat16, seed=8)
+    _, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    first = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    ws = torch.full((fa.layer_norm_ws_bytes(T, N),), 255, dtype=torch.uint8, device="cuda")
+    again = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds, ws=ws)
+    assert all(torch.equal(a, c) for a, c in zip(first, again))
+
+
+def test_many_rows_and_offsets_past_32_bits():
+    """2^31 elements and more: rows beyond the 32-bit range of an element
+    offset, sampled."""
+    need_gpu()
+    T, N = 70000, 32768
+    x = torch.empty(T, N, dtype=torch.bfloat16, device="cuda").normal_()
+    w = torch.linspace(0.5, 1.5, N, device="cuda").bfloat16()
+    y, mean, rstd = fa.layer_norm_fwd(x, w, None, EPS, out=x.clone())
+    rows = [0, 65535, 65536, T - 1]
+    check_fwd(x[rows], w, None, True, y[rows], mean[rows], rstd[rows])
+    dx, _, _ = fa.layer_norm_bwd(y, x, w, mean, rstd, dx=y.clone())
+    c = cpu(y[rows], x[rows], w, mean[rows], rstd[rows])
+    (dxe, _, _), (bx, _, _) = R.norm_bwd(*c, True)
+    R.check("dx", dx[rows], dxe, bx, dx.dtype)
+
+
+def test_another_stream():
+    need_gpu()
+    (x, r, dy, ds), w, b = inputs(500, 4096, torch.bfloat16, seed=2)
+    want = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+    wantb = fa.dropout_add_layer_norm_bwd(dy, ds, want[1], w, want[2], want[3], 0.1, SEED)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+        gotb = fa.dropout_add_layer_norm_bwd(dy, ds, got[1], w, got[2], got[3], 0.1, SEED)
+    side.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got + gotb, want + wantb))
+
+
+def test_captured_graph_draws_a_new_mask_at_each_replay():
+    need_gpu()
+    (x, r, dy, ds), w, b = inputs(64, 4096, torch.bfloat16, seed=2)
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED, step=step)
+        g = fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED, step=step)
+    seen = []
+    for k in (0, 1, 2 ** 40):
+        step.fill_(k)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED + k)
+        wantb = fa.dropout_add_layer_norm_bwd(dy, ds, want[1], w, want[2], want[3], 0.1, SEED + k)
+        assert all(torch.equal(a, c) for a, c in zip(f + g, want + wantb))
+        seen.append(f[1].clone())
+    assert not torch.equal(seen[0], seen[1])
