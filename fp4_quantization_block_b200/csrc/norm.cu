@@ -228,6 +228,328 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------ rows kept on the chip ---
+// How a launch lays rows over threads (host rule: choose_layout).
+struct Layout {
+  int warps;   // of a team (one row)
+  int teams;   // of a CTA
+  int stages;  // of the ring
+  bool words;  // 16-bit rows start on 4-byte boundaries (unaligned kernels)
+};
+
+// Each team takes every (gridDim.x * teams)-th row.  CH chunks per thread.
+template <typename T, int CH, bool VEC, bool FUSED>
+__global__ void __launch_bounds__(512) norm_fwd_kernel(const FwdParams p, const Layout g) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][16];
+  constexpr int A = FUSED ? 2 : 1;
+  const int lane = threadIdx.x & 31, cta_warp = threadIdx.x >> 5;
+  const int team = cta_warp / g.warps, warp = cta_warp - team * g.warps;
+  const int cols = (int)p.N;
+  constexpr int kTile = 256, kStage = A * CH * kTile;
+  T *ring = reinterpret_cast<T *>(smem) + (size_t)cta_warp * g.stages * kStage;
+  float *red0 = &red[0][team * g.warps], *red1 = &red[1][team * g.warps];
+  const int64_t step = (int64_t)gridDim.x * g.teams;
+  int64_t row = (int64_t)blockIdx.x * g.teams + team;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  auto fill = [&](int stage, int64_t r) {
+    if (r < p.T) {
+      T *t = ring + stage * kStage;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int cb = (j * g.warps + warp) * kTile;
+        fill_tile<T, VEC>(t + j * kTile, static_cast<const T *>(p.x) + r * p.ldx, cb, cols, g.words, lane);
+        if constexpr (FUSED)
+          fill_tile<T, VEC>(t + (CH + j) * kTile, static_cast<const T *>(p.res) + r * p.ldres, cb, cols,
+                            g.words, lane);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s < g.stages - 1; ++s) fill(s, row + s * step);
+
+  const uint64_t key = FUSED ? p.drop.key() : 0ull;
+  const Vec<T> wv{p.w, p.w_f32}, bv{p.b, p.w_f32};
+  float w[CH][8], b[CH][8];
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (j * g.warps + warp) * kTile + 8 * lane + i;
+      w[j][i] = c < cols ? wv.at(c) : 0.0f;
+      b[j][i] = c < cols && p.b ? bv.at(c) : 0.0f;
+    }
+  const float n = (float)cols;
+
+  int stage = 0;
+  for (; row < p.T; row += step) {
+    __syncwarp();  // the stage filled next was read by the whole warp
+    const int next = stage + g.stages - 1;
+    fill(next >= g.stages ? next - g.stages : next, row + (g.stages - 1) * step);
+    cp_async_wait(g.stages - 1);
+    __syncwarp();
+    T *t = ring + stage * kStage;
+    float v[CH][8], sum[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int cb = (j * g.warps + warp) * kTile, c = cb + 8 * lane;
+      read_tile<T, VEC>(t + j * kTile, c, cols, lane, v[j]);
+      if constexpr (FUSED) {
+        float r[8];
+        drop8(p.drop, key, (uint32_t)row, (uint32_t)c, v[j]);
+        read_tile<T, VEC>(t + (CH + j) * kTile, c, cols, lane, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] += r[i];
+        round8<T>(v[j]);
+        store_tile<T, VEC>(t + j * kTile, static_cast<T *>(p.s) + row * p.lds, cb, cols, g.words, lane,
+                           v[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += v[j][i];
+    }
+    float mean = 0.0f;
+    if (p.center) {
+      team_sum<1>(sum, red0, g.warps, warp, lane, 1 + team);
+      mean = sum[0] / n;
+    }
+    float m2[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * g.warps + warp) * kTile + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[j][i] -= mean;
+        if ((VEC ? c : c + i) < cols) m2[0] = fmaf(v[j][i], v[j][i], m2[0]);
+      }
+    }
+    team_sum<1>(m2, red1, g.warps, warp, lane, 1 + team);
+    const float rstd = __frsqrt_rn(m2[0] / n + p.eps);
+    if (warp == 0 && lane == 0) {
+      if (p.center) p.mean[row] = mean;
+      p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int cb = (j * g.warps + warp) * kTile;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = fmaf(v[j][i] * rstd, w[j][i], b[j][i]);
+      store_tile<T, VEC>(t + j * kTile, static_cast<T *>(p.y) + row * p.ldy, cb, cols, g.words, lane, v[j]);
+    }
+    // without centring the one barrier of a row does not keep the next row's
+    // sums from this row's readers
+    if (!p.center && g.warps > 1) {
+      float *q = red0;
+      red0 = red1;
+      red1 = q;
+    }
+    stage = stage + 1 == g.stages ? 0 : stage + 1;
+  }
+}
+
+// dx of a team's rows; dw and db of its columns stay in registers over its
+// rows, are added up over the CTA's teams in order and go to the CTA's
+// partial sums.
+template <typename T, int CH, bool VEC, bool FUSED>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdParams p, const Layout g) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, cta_warp = threadIdx.x >> 5;
+  const int team = cta_warp / g.warps, warp = cta_warp - team * g.warps;
+  const int cols = (int)p.N;
+  constexpr int kTile = 256;
+  constexpr int kHead = 16 / (int)sizeof(T);  // a stage starts with the row's mean and rstd
+  const int arrays = p.ds ? 3 : 2, stage_len = arrays * CH * kTile + kHead;
+  T *ring = reinterpret_cast<T *>(smem) + (size_t)cta_warp * g.stages * stage_len;
+  float *red0 = &red[0][2 * team * g.warps], *red1 = &red[1][2 * team * g.warps];
+  const int64_t step = (int64_t)gridDim.x * g.teams;
+  int64_t row = (int64_t)blockIdx.x * g.teams + team;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  auto fill = [&](int stage, int64_t r) {
+    if (r < p.T) {
+      T *t = ring + stage * stage_len;
+      if (lane == 0) {
+        if (p.center) cp_async4(t, p.mean + r);
+        cp_async4(reinterpret_cast<float *>(t) + 1, p.rstd + r);
+      }
+      t += kHead;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        const int cb = (j * g.warps + warp) * kTile;
+        fill_tile<T, VEC>(t + j * kTile, static_cast<const T *>(p.x) + r * p.ldx, cb, cols, g.words, lane);
+        fill_tile<T, VEC>(t + (CH + j) * kTile, static_cast<const T *>(p.dy) + r * p.lddy, cb, cols,
+                          g.words, lane);
+        if (p.ds)
+          fill_tile<T, VEC>(t + (2 * CH + j) * kTile, static_cast<const T *>(p.ds) + r * p.ldds, cb, cols,
+                            g.words, lane);
+      }
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s < g.stages - 1; ++s) fill(s, row + s * step);
+
+  const uint64_t key = FUSED ? p.drop.key() : 0ull;
+  const Vec<T> wv{p.w, p.w_f32};
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = (j * g.warps + warp) * kTile + 8 * lane + i;
+      w[j][i] = c < cols ? wv.at(c) : 0.0f;
+      dw[j][i] = db[j][i] = 0.0f;
+    }
+  const float inv_n = 1.0f / (float)cols;
+
+  int stage = 0;
+  for (; row < p.T; row += step) {
+    __syncwarp();  // the stage filled next was read by the whole warp
+    const int next = stage + g.stages - 1;
+    fill(next >= g.stages ? next - g.stages : next, row + (g.stages - 1) * step);
+    cp_async_wait(g.stages - 1);
+    __syncwarp();
+    T *t = ring + stage * stage_len;
+    const float mean = p.center ? reinterpret_cast<const float *>(t)[0] : 0.0f;
+    const float rstd = reinterpret_cast<const float *>(t)[1];
+    t += kHead;
+    float c12[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = (j * g.warps + warp) * kTile + 8 * lane;
+      float x[8], dy[8];
+      read_tile<T, VEC>(t + j * kTile, c, cols, lane, x);
+      read_tile<T, VEC>(t + (CH + j) * kTile, c, cols, lane, dy);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = (x[i] - mean) * rstd, gi = dy[i] * w[j][i];
+        dw[j][i] = fmaf(dy[i], xh, dw[j][i]);
+        db[j][i] += dy[i];
+        c12[0] += gi;
+        c12[1] = fmaf(gi, xh, c12[1]);
+      }
+    }
+    team_sum<2>(c12, red0, g.warps, warp, lane, 1 + team);
+    {
+      float *q = red0;
+      red0 = red1;
+      red1 = q;
+    }
+    const float c1 = p.center ? c12[0] * inv_n : 0.0f, c2 = c12[1] * inv_n;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int cb = (j * g.warps + warp) * kTile, c = cb + 8 * lane;
+      float x[8], dy[8], d[8];
+      read_tile<T, VEC>(t + j * kTile, c, cols, lane, x);
+      read_tile<T, VEC>(t + (CH + j) * kTile, c, cols, lane, dy);
+      if (p.ds) read_tile<T, VEC>(t + (2 * CH + j) * kTile, c, cols, lane, d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = (x[i] - mean) * rstd;
+        x[i] = fmaf(-xh, c2, dy[i] * w[j][i] - c1) * rstd;
+        if (p.ds) x[i] += d[i];
+      }
+      if constexpr (FUSED) {
+        store_tile<T, VEC>(t + j * kTile, static_cast<T *>(p.dres) + row * p.lddres, cb, cols, g.words,
+                           lane, x);
+        drop8(p.drop, key, (uint32_t)row, (uint32_t)c, x);
+      }
+      store_tile<T, VEC>(t + j * kTile, static_cast<T *>(p.dx) + row * p.lddx, cb, cols, g.words, lane, x);
+    }
+    stage = stage + 1 == g.stages ? 0 : stage + 1;
+  }
+
+  // the teams' sums, through the ring's memory
+  float *out = p.partials + (int64_t)blockIdx.x * 2 * p.N;
+  if (g.teams > 1) {
+    cp_async_wait(0);
+    __syncthreads();
+    const int width = g.warps * CH * kTile;
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * g.warps + warp) * kTile + 8 * lane + i;
+        sums[(2 * team) * width + c] = dw[j][i];
+        sums[(2 * team + 1) * width + c] = db[j][i];
+      }
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+      float a = 0.0f, d = 0.0f;
+      for (int k = 0; k < g.teams; ++k) {
+        a += sums[2 * k * width + c];
+        d += sums[(2 * k + 1) * width + c];
+      }
+      out[c] = a;
+      out[p.N + c] = d;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = (j * g.warps + warp) * kTile + 8 * lane + i;
+        if (c < cols) {
+          out[c] = dw[j][i];
+          out[p.N + c] = db[j][i];
+        }
+      }
+  }
+}
+
+constexpr int kSms = 148;
+constexpr size_t kMaxSmem = 227 * 1024 - 1024;  // the static arrays' share left out
+
+// Chunks per thread, warps per row, rows per CTA and stages for rows of N
+// values whose stage takes `arrays` x N values of `size` bytes, at most
+// `threads` threads a CTA; 0 chunks: the row does not fit.
+struct Choice {
+  int ch = 0;
+  Layout g = {};
+  size_t smem = 0;
+};
+Choice choose_layout(int64_t T, int64_t N, int arrays, int size, int head, int threads, size_t budget,
+                     bool sums) {
+  Choice c;
+  if (N > 16384) return c;
+  const int chunks = (int)((N + 7) / 8);
+  c.ch = chunks <= 32 ? 1 : chunks <= 1024 ? 2 : 4;
+  c.g.warps = (chunks + 32 * c.ch - 1) / (32 * c.ch);
+  c.g.teams = threads / 32 / c.g.warps;
+  if (c.g.teams > 8) c.g.teams = 8;
+  if (c.g.teams < 1) c.g.teams = 1;
+  // few rows: one team per SM first
+  while (c.g.teams > 1 && T <= (int64_t)kSms * (c.g.teams - 1)) --c.g.teams;
+  const int warps = c.g.warps * c.g.teams;
+  const size_t stage = (size_t)warps * ((size_t)arrays * c.ch * 256 * size + head);
+  const size_t least = sums && c.g.teams > 1 ? (size_t)warps * c.ch * 256 * 8 : 0;
+  c.g.stages = (int)(budget / stage);
+  if (c.g.stages > kMaxStages) c.g.stages = kMaxStages;
+  if (c.g.stages < 1 && stage <= kMaxSmem) c.g.stages = 1;
+  if (c.g.stages < 1) {
+    c.ch = 0;
+    return c;
+  }
+  c.smem = c.g.stages * stage;
+  if (c.smem < least) c.smem = least;
+  return c;
+}
+
+template <typename K, typename P>
+cudaError_t launch_rows(K kern, const P &p, const Choice &c, int ctas_per_sm, cudaStream_t st) {
+  if (c.smem > 40 * 1024) {  // static shared memory counts towards the default 48 KB too
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t need = (p.T + c.g.teams - 1) / c.g.teams, most = (int64_t)kSms * ctas_per_sm;
+  return launch_pdl(kern, dim3((unsigned)(need < most ? need : most)),
+                    dim3(32 * c.g.warps * c.g.teams), c.smem, st, p, c.g);
+}
+
 Drop make_drop(const DropArgs &d) { return {d.seed, d.step, d.threshold, d.scale}; }
 
 inline bool vec_ok(const void *p, int64_t ld) {
@@ -243,29 +565,70 @@ cudaError_t by_type(int dtype, F &&f) {
   }
 }
 
-unsigned row_ctas(int64_t T) { return (unsigned)(T < 148 * 4 ? T : 148 * 4); }
-// row groups of the dw pass, so that its CTAs fill the GPU twice over
+unsigned row_ctas(int64_t T) { return (unsigned)(T < kSms * 4 ? T : kSms * 4); }
+// row groups of the wide dw pass, so that its CTAs fill the GPU twice over
 int wide_splits(int64_t T, int64_t N) {
   const int64_t strips = (N + 255) / 256, groups = (T + 7) / 8;
-  int64_t s = (148 * 8 + strips - 1) / strips;
+  int64_t s = (kSms * 8 + strips - 1) / strips;
   s = s < groups ? s : groups;
   return (int)(s < 1 ? 1 : s > kMaxNormPartials ? kMaxNormPartials : s);
+}
+inline bool word_ok(const void *p, int64_t ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && ld % 2 == 0;
+}
+
+template <typename T, bool VEC, bool FUSED>
+cudaError_t fwd(const FwdParams &p, bool words, cudaStream_t st) {
+  Choice c = choose_layout(p.T, p.N, FUSED ? 2 : 1, (int)sizeof(T), 0, 256, 100 * 1024, false);
+  c.g.words = words;
+  const int per_sm = c.g.warps * c.g.teams > 8 ? 1 : 2;
+  switch (c.ch) {
+    case 1: return launch_rows(norm_fwd_kernel<T, 1, VEC, FUSED>, p, c, per_sm, st);
+    case 2: return launch_rows(norm_fwd_kernel<T, 2, VEC, FUSED>, p, c, per_sm, st);
+    case 4: return launch_rows(norm_fwd_kernel<T, 4, VEC, FUSED>, p, c, per_sm, st);
+  }
+  return launch_pdl(norm_fwd_wide_kernel<T, VEC, FUSED>, dim3(row_ctas(p.T)), dim3(kWideThreads), 0, st, p);
+}
+// Partial sums of dw and db; *n of them.
+template <typename T, bool VEC, bool FUSED>
+cudaError_t bwd(const BwdParams &p, bool words, int *n, cudaStream_t st) {
+  Choice c = choose_layout(p.T, p.N, p.ds ? 3 : 2, (int)sizeof(T), 16, 512, kMaxSmem, true);
+  c.g.words = words;
+  if (c.ch) {
+    const int64_t need = (p.T + c.g.teams - 1) / c.g.teams;
+    *n = (int)(need < kSms ? need : kSms);
+  }
+  switch (c.ch) {
+    case 1: return launch_rows(norm_bwd_kernel<T, 1, VEC, FUSED>, p, c, 1, st);
+    case 2: return launch_rows(norm_bwd_kernel<T, 2, VEC, FUSED>, p, c, 1, st);
+    case 4: return launch_rows(norm_bwd_kernel<T, 4, VEC, FUSED>, p, c, 1, st);
+  }
+  *n = wide_splits(p.T, p.N);
+  // dw first: dx may take the place of dy or x
+  const cudaError_t e = launch_pdl(norm_dw_wide_kernel<T, VEC>, dim3((unsigned)((p.N + 255) / 256), (unsigned)*n),
+                                   dim3(256), 0, st, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_dx_wide_kernel<T, VEC, FUSED>, dim3(row_ctas(p.T)), dim3(kWideThreads), 0, st, p);
 }
 
 }  // namespace
 
-int norm_partials_count(int64_t T, int64_t N) { return wide_splits(T, N); }
+int norm_partials_count(int64_t T, int64_t N) {
+  const int w = wide_splits(T, N);
+  return w > kSms ? w : kSms;
+}
 
 cudaError_t launch_norm_fwd(const NormFwdArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.x, a.ldx) && vec_ok(a.y, a.ldy) &&
                    (!a.fused || (vec_ok(a.res, a.ldres) && vec_ok(a.s, a.lds)));
+  const bool words = word_ok(a.x, a.ldx) && word_ok(a.y, a.ldy) &&
+                     (!a.fused || (word_ok(a.res, a.ldres) && word_ok(a.s, a.lds)));
   const FwdParams p = {a.x, a.res, a.ldx, a.ldres, a.T,   a.N,    a.w,    a.b, a.w_f32, a.center,
                        a.eps, a.y, a.s,   a.ldy,   a.lds, a.mean, a.rstd, make_drop(a.drop)};
   return by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    auto kern = a.fused ? (vec ? norm_fwd_wide_kernel<T, true, true> : norm_fwd_wide_kernel<T, false, true>)
-                        : (vec ? norm_fwd_wide_kernel<T, true, false> : norm_fwd_wide_kernel<T, false, false>);
-    return launch_pdl(kern, dim3(row_ctas(a.T)), dim3(kWideThreads), 0, st, p);
+    return a.fused ? (vec ? fwd<T, true, true>(p, words, st) : fwd<T, false, true>(p, words, st))
+                   : (vec ? fwd<T, true, false>(p, words, st) : fwd<T, false, false>(p, words, st));
   });
 }
 
@@ -273,24 +636,20 @@ cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.dy, a.lddy) && vec_ok(a.x, a.ldx) &&
                    vec_ok(a.dx, a.lddx) && (!a.ds || vec_ok(a.ds, a.ldds)) &&
                    (!a.fused || vec_ok(a.dres, a.lddres));
+  const bool words = word_ok(a.dy, a.lddy) && word_ok(a.x, a.ldx) && word_ok(a.dx, a.lddx) &&
+                     (!a.ds || word_ok(a.ds, a.ldds)) && (!a.fused || word_ok(a.dres, a.lddres));
   const BwdParams p = {a.dy, a.x, a.ds, a.lddy, a.ldx, a.ldds, a.T, a.N, a.w, a.w_f32, a.center,
                        a.mean, a.rstd, a.dx, a.dres, a.lddx, a.lddres, a.partials,
                        make_drop(a.drop)};
-  const int splits = wide_splits(a.T, a.N);
-  cudaError_t e = by_type(a.dtype, [&](auto t) {
+  int n = 0;
+  const cudaError_t e = by_type(a.dtype, [&](auto t) {
     using T = decltype(t);
-    auto kern = a.fused ? (vec ? norm_dx_wide_kernel<T, true, true> : norm_dx_wide_kernel<T, false, true>)
-                        : (vec ? norm_dx_wide_kernel<T, true, false> : norm_dx_wide_kernel<T, false, false>);
-    // dw first: dx may take the place of dy or x
-    auto dwk = vec ? norm_dw_wide_kernel<T, true> : norm_dw_wide_kernel<T, false>;
-    const cudaError_t e1 =
-        launch_pdl(dwk, dim3((unsigned)((a.N + 255) / 256), (unsigned)splits), dim3(256), 0, st, p);
-    if (e1 != cudaSuccess) return e1;
-    return launch_pdl(kern, dim3(row_ctas(a.T)), dim3(kWideThreads), 0, st, p);
+    return a.fused ? (vec ? bwd<T, true, true>(p, words, &n, st) : bwd<T, false, true>(p, words, &n, st))
+                   : (vec ? bwd<T, true, false>(p, words, &n, st) : bwd<T, false, false>(p, words, &n, st));
   });
   if (e != cudaSuccess) return e;
   return launch_pdl(norm_colsum_kernel, dim3((unsigned)((a.N + 31) / 32), a.db ? 2u : 1u), dim3(256), 0,
-                    st, a.partials, splits, a.N, a.dw, a.db);
+                    st, a.partials, n, a.N, a.dw, a.db);
 }
 
 }  // namespace fa4

@@ -175,5 +175,144 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// ----------------------------------------------- rows kept on the chip ---
+// A team of W warps holds one row: warp w's j-th tile is the 256 columns from
+// 256 (j W + w), lane l's chunk the eight from 8 l in it.  Tiles come through
+// a ring of stages in shared memory, private to the warp, filled by
+// asynchronous copies several rows ahead, so that what is in flight does not
+// depend on registers; a warp waits only for its own copies.
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest n groups of this thread have arrived.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  if (n >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1)
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+constexpr int kMaxStages = 4;
+
+// A warp's copy of columns cb .. cb+255 (those below cols) of a row into a
+// tile.  VEC: 16-byte copies.  Otherwise 4-byte ones where the row allows
+// them (`words`: binary32, or 16-bit rows that start on 4-byte boundaries),
+// and plain loads for 16-bit rows that do not.  Visible to the warp after
+// cp_async_wait and __syncwarp.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fill_tile(T *tile, const T *row, int cb, int cols, bool words, int lane) {
+  constexpr int kPer16 = 16 / (int)sizeof(T), kPer4 = 4 / (int)sizeof(T);
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 256 / (32 * kPer16); ++i) {
+      const int e = (32 * i + lane) * kPer16;
+      if (cb + e < cols) cp_async16(tile + e, row + cb + e);
+    }
+  } else if (sizeof(T) == 4 || words) {
+#pragma unroll
+    for (int i = 0; i < 256 / (32 * kPer4); ++i) {
+      const int e = (32 * i + lane) * kPer4;
+      if (cb + e + kPer4 <= cols)
+        cp_async4(tile + e, row + cb + e);
+      else if (cb + e < cols)
+        tile[e] = row[cb + e];
+    }
+  } else {
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (cb + 32 * i + lane < cols) v[i] = row[cb + 32 * i + lane];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (cb + 32 * i + lane < cols) tile[32 * i + lane] = v[i];
+  }
+}
+// A lane's chunk of a tile at column c = cb + 8 lane, zeros from cols on.
+template <typename T, bool VEC>
+__device__ __forceinline__ void read_tile(const T *tile, int c, int cols, int lane, float (&f)[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4 *>(tile + 8 * lane)[i];
+  unpack8(r, f);
+  if (VEC) {
+    if (c >= cols)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? f[i] : 0.0f;
+  }
+}
+// Stores the warp's 256 columns from cb, lane l holding the eight from 8 l:
+// 16-bit chunks directly, the others through `tile` (which the warp has
+// finished reading), so that neighbouring lanes write neighbouring bytes.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_tile(T *tile, T *row, int cb, int cols, bool words, int lane,
+                                           const float (&f)[8]) {
+  constexpr int kPer16 = 16 / (int)sizeof(T), kPer4 = 4 / (int)sizeof(T);
+  Raw8<T> r;
+  pack8(f, r);
+  if constexpr (VEC && sizeof(T) == 2) {
+    if (cb + 8 * lane < cols) *reinterpret_cast<uint4 *>(row + cb + 8 * lane) = r.v[0];
+    return;
+  }
+  __syncwarp();  // the tile's last readers
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(tile + 8 * lane)[i] = r.v[i];
+  __syncwarp();
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 256 / (32 * kPer16); ++i) {
+      const int e = (32 * i + lane) * kPer16;
+      if (cb + e < cols) *reinterpret_cast<uint4 *>(row + cb + e) = *reinterpret_cast<const uint4 *>(tile + e);
+    }
+  } else if (sizeof(T) == 4 || words) {
+#pragma unroll
+    for (int i = 0; i < 256 / (32 * kPer4); ++i) {
+      const int e = (32 * i + lane) * kPer4;
+      if (cb + e + kPer4 <= cols)
+        *reinterpret_cast<uint32_t *>(row + cb + e) = *reinterpret_cast<const uint32_t *>(tile + e);
+      else if (cb + e < cols)
+        row[cb + e] = tile[e];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = 32 * i + lane;
+      if (cb + e < cols) row[cb + e] = tile[e];
+    }
+  }
+}
+
+// Sums of K values over a team of W warps, the same bits in every thread: a
+// butterfly in the warp, then over the warps' sums.  `red` holds W x K floats;
+// two uses of one buffer need a barrier of the team between them.
+template <int K>
+__device__ __forceinline__ void team_sum(float (&v)[K], float *red, int W, int warp, int lane, int bar) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
+  if (W == 1) return;
+  if (lane == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) red[warp * K + k] = v[k];
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
+  const int pow2 = W > 8 ? (W > 16 ? 32 : 16) : (W > 4 ? 8 : (W > 2 ? 4 : 2)), l = lane & (pow2 - 1);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = l < W ? red[l * K + k] : 0.0f;
+  for (int o = pow2 >> 1; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+}
+
 }  // namespace rows
 }  // namespace fa4
