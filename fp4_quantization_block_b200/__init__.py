@@ -128,11 +128,18 @@ def _check(status: int, what: str):
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without building a Stream object around it (a
+# tenth of a small call's time), where this torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _on_tensor_device(fn):
@@ -144,9 +151,11 @@ def _on_tensor_device(fn):
 
     @functools.wraps(fn)
     def wrapped(*args, **kwargs):
-        for a in list(args) + list(kwargs.values()):
+        for a in (*args, *kwargs.values()):
             t = a.payload if isinstance(a, QTensor) else a
             if isinstance(t, torch.Tensor) and t.is_cuda:
+                if t.get_device() == torch.cuda.current_device():
+                    return fn(*args, **kwargs)
                 with torch.cuda.device(t.device):
                     return fn(*args, **kwargs)
         return fn(*args, **kwargs)
@@ -593,17 +602,22 @@ def _rows(x: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
     if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
         raise ValueError(f"{name} must be a {list(like.shape)} {like.dtype} tensor on {like.device}")
     rows, cols = x.shape
-    if cols != 1 and x.stride(1) != 1:
+    ld, unit = x.stride()
+    if unit != 1 and cols != 1:
         raise ValueError(f"{name} must have unit column stride")
     if rows == 1:
         return -(-cols // 8) * 8  # one row: its stride means nothing
-    if x.stride(0) < cols:
-        raise ValueError(f"{name} has overlapping rows (row stride {x.stride(0)} < {cols})")
-    return x.stride(0)
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows (row stride {ld} < {cols})")
+    return ld
 
 
 def _new_rows(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _new_f32(x: torch.Tensor, n: int) -> torch.Tensor:
+    return x.new_empty(n, dtype=torch.float32)
 
 
 def _vector(v: torch.Tensor, n: int, dtypes: tuple, device, name: str):
@@ -636,13 +650,13 @@ def _step(step, x):
 def _grads(dweight, dbias, bias_grad, x):
     n, dev = x.shape[1], x.device
     if dweight is None:
-        dweight = torch.empty(n, dtype=torch.float32, device=dev)
+        dweight = _new_f32(x, n)
     else:
         _vector(dweight, n, (torch.float32,), dev, "dweight")
     if not bias_grad:
         return dweight, None
     if dbias is None:
-        dbias = torch.empty(n, dtype=torch.float32, device=dev)
+        dbias = _new_f32(x, n)
     else:
         _vector(dbias, n, (torch.float32,), dev, "dbias")
     return dweight, dbias
@@ -656,7 +670,7 @@ def layer_norm_ws_bytes(rows: int, cols: int) -> int:
 
 def _norm_ws(ws, x):
     if ws is None:  # nothing in it has to start at zero
-        return torch.empty(layer_norm_ws_bytes(*x.shape), dtype=torch.uint8, device=x.device)
+        return x.new_empty(layer_norm_ws_bytes(*x.shape), dtype=torch.uint8)
     if ws.device != x.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous uint8 tensor on {x.device}")
     return ws
@@ -675,8 +689,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     y = _new_rows(x) if out is None else out
     ldy = _rows(y, "out", x)
     T, N = x.shape
-    mean = torch.empty(T, dtype=torch.float32, device=x.device) if center else None
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    mean, rstd = _new_f32(x, T) if center else None, _new_f32(x, T)
     _check(lib().fa4_layernorm_fwd(_ptr(x), ldx, T, N, DTYPE[x.dtype], _ptr(weight), _ptr(bias), wd,
                                    eps, 1 if center else 0, _ptr(y), ldy, _ptr(mean), _ptr(rstd),
                                    _stream(x.device)), "fa4_layernorm_fwd")
@@ -760,8 +773,7 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
     s = _new_rows(x) if s is None else s
     ldy, lds = _rows(y, "out", x), _rows(s, "s", x)
     T, N = x.shape
-    mean = torch.empty(T, dtype=torch.float32, device=x.device) if center else None
-    rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    mean, rstd = _new_f32(x, T) if center else None, _new_f32(x, T)
     _check(lib().fa4_dropout_add_layernorm_fwd(
         _ptr(x), ldx, _ptr(residual), ldr, T, N, DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF,
         _step(step, x), _ptr(weight), _ptr(bias), wd, eps, 1 if center else 0, _ptr(s), lds, _ptr(y),
@@ -810,7 +822,7 @@ def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = Non
     if F2 % 2 or dh.shape != (T, F2 // 2) or dh.device != z.device:
         raise ValueError(f"z must hold gate and up halves and dh must be [{T}, {F2 // 2}] on {z.device}")
     if out is None:
-        out = torch.empty((T, F2), dtype=torch.bfloat16, device=z.device)
+        out = _new_rows(z)
     else:
         _check_out(out, (T, F2), (torch.bfloat16,), z.device, "out", row_stride=True)
     _check(lib().fa4_swiglu_bwd(_ptr(z), ldz, _ptr(dh), lddh, T, F2 // 2, _ptr(out), out.stride(0),

@@ -2,6 +2,11 @@
 // residual addition: y = [res +] (kept ? x * scale : 0), the mask computed
 // from (key, row, column) where it is needed (rows.cuh) and never stored.
 // The backward pass is the same map of dy under the same key.
+//
+// Bound by memory: two or three accesses of an element against some five
+// integer instructions for its share of the generator.  Each thread has all
+// its loads in flight before it computes, and the grid covers the matrix
+// once.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -14,33 +19,148 @@ namespace {
 
 using namespace rows;
 
+#ifndef DROP_U
+#define DROP_U 2
+#endif
+constexpr int kThreads = 256;
+
 struct DropoutParams {
   const void *x, *res;
   void *y;
-  int64_t ldx, ldres, ldy, T, N, chunks;
+  int64_t ldx, ldres, ldy, T, N;
+  int64_t units;  // of the matrix: chunks of eight columns, or warps' tiles
+  Divisor per_row;
   Drop drop;
 };
 
-// One chunk of eight columns per thread and step.  y may be x or res itself:
-// a thread reads its elements before it writes them.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams p) {
+// Row and unit in its row of the n-th unit of the CTA's, which start at
+// `first` = (row0, unit0).
+__device__ __forceinline__ void place(const DropoutParams &p, int64_t row0, uint32_t unit0, uint32_t n,
+                                      int64_t &row, uint32_t &unit) {
+  const uint32_t u = unit0 + n, q = p.per_row.quotient(u);
+  row = row0 + q;
+  unit = u - q * p.per_row.d;
+}
+
+// Rows on 16-byte boundaries, N a multiple of eight.  A warp step is 32
+// consecutive chunks; a lane of a 16-bit type has one of them, a lane of
+// binary32 the even or odd halves of two (16-byte accesses that are
+// consecutive over the lanes).  y may be x or res itself: a thread reads its
+// elements before it writes them.
+template <typename T, int kUnroll>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
+  constexpr int H = sizeof(T) / 2;  // 16-byte pieces of a lane
+  constexpr int kPer16 = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
   const uint64_t key = p.drop.key();
-  const int64_t total = p.T * p.chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / p.chunks, c = 8 * (i - r * p.chunks);
-    float f[8];
-    load8<T, VEC>(static_cast<const T *>(p.x) + r * p.ldx, c, p.N, f);
-    drop8(p.drop, key, (uint32_t)r, (uint32_t)c, f);
-    if (p.res) {
-      float g[8];
-      load8<T, VEC>(static_cast<const T *>(p.res) + r * p.ldres, c, p.N, g);
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
+  const int64_t row0 = p.units < (int64_t(1) << 31) ? p.per_row.quotient((uint32_t)first) : first / p.per_row.d;
+  const uint32_t unit0 = (uint32_t)(first - row0 * p.per_row.d);
+  uint4 x[kUnroll][H], r[kUnroll][H];
+  // the chunk of the CTA's that a lane's h-th piece of step k lies in
+  auto chunk = [&](int k, int h) {
+    const uint32_t warp0 = k * kThreads + (threadIdx.x & ~31u);
+    return H == 1 ? warp0 + lane : warp0 + 16 * h + (lane >> 1);
+  };
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += g[j];
+  for (int k = 0; k < kUnroll; ++k)
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (first + chunk(k, h) < p.units) {
+        int64_t row;
+        uint32_t unit;
+        place(p, row0, unit0, chunk(k, h), row, unit);
+        const int64_t c = 8 * (int64_t)unit + (H == 2 ? kPer16 * (lane & 1) : 0);
+        x[k][h] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + row * p.ldx + c));
+        if (p.res)
+          r[k][h] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.res) + row * p.ldres + c));
+      }
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    // the block whose bits this lane computes: its chunk, or (binary32) the
+    // first or the second of the two that it shares with its neighbour
+    int64_t row;
+    uint32_t unit;
+    place(p, row0, unit0, chunk(k, H == 1 ? 0 : lane & 1), row, unit);
+    uint32_t w[4];
+    if (p.drop.threshold) {
+      const u32x4 b = philox(unit, (uint32_t)row, 0u, kDropTag, (uint32_t)key, (uint32_t)(key >> 32));
+      w[0] = b.x, w[1] = b.y, w[2] = b.z, w[3] = b.w;
+      if constexpr (H == 2) share_bits(b, lane, w);
     }
-    store8<T, VEC>(static_cast<T *>(p.y) + r * p.ldy, c, p.N, f);
+    Raw8<T> raw;
+    uint64_t f[4];
+#pragma unroll
+    for (int h = 0; h < H; ++h) raw.v[h] = x[k][h];
+    unpack8(raw, f);
+    if (p.drop.threshold) drop_pairs(p.drop, w, f);
+    if (p.res) {
+      uint64_t g[4];
+#pragma unroll
+      for (int h = 0; h < H; ++h) raw.v[h] = r[k][h];
+      unpack8(raw, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = f2_add(f[i], g[i]);
+    }
+    pack8(f, raw);
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (first + chunk(k, h) < p.units) {
+        place(p, row0, unit0, chunk(k, h), row, unit);
+        const int64_t c = 8 * (int64_t)unit + (H == 2 ? kPer16 * (lane & 1) : 0);
+        *reinterpret_cast<uint4 *>(static_cast<T *>(p.y) + row * p.ldy + c) = raw.v[h];
+      }
+  }
+}
+
+// Any rows: a warp takes 256 columns of a row, element by element in column
+// order (lane l the columns l, 32 + l, ...), so that its accesses are
+// consecutive; lane l computes the bits of block l of the tile, and each
+// element takes its bit from the lane that has it.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dropout_any_kernel(const DropoutParams p) {
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / 32);
+  const int64_t row0 = p.units < (int64_t(1) << 31) ? p.per_row.quotient((uint32_t)first) : first / p.per_row.d;
+  const uint32_t warp = threadIdx.x >> 5;
+  if (first + warp >= p.units) return;
+  int64_t row;
+  uint32_t unit;
+  place(p, row0, (uint32_t)(first - row0 * p.per_row.d), warp, row, unit);
+  const int64_t col = (int64_t)unit * kTile + lane;
+  const T *x = static_cast<const T *>(p.x) + row * p.ldx + col;
+  const T *res = static_cast<const T *>(p.res) + row * p.ldres + col;
+  T *y = static_cast<T *>(p.y) + row * p.ldy + col;
+  T v[8], r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + 32 * i < p.N) {
+      v[i] = x[32 * i];
+      if (p.res) r[i] = res[32 * i];
+    }
+  uint32_t bits = 0xFFu;  // which of the block's eight are kept
+  if (p.drop.threshold) {
+    const uint64_t key = p.drop.key();
+    const u32x4 b = philox(unit * (kTile / 8) + lane, (uint32_t)row, 0u, kDropTag, (uint32_t)key,
+                           (uint32_t)(key >> 32));
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w}, t = p.drop.threshold << 16;
+    bits = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bits |= ((w[i] << 16) >= t ? 1u << (2 * i) : 0u) | (w[i] >= t ? 2u << (2 * i) : 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t block = __shfl_sync(0xFFFFFFFFu, bits, 4 * i + (lane >> 3));
+    if (col + 32 * i < p.N) {
+      float f = (block >> (lane & 7)) & 1u ? to_float(v[i]) * p.drop.scale : 0.0f;
+      if (p.res) f += to_float(r[i]);
+      y[32 * i] = from_float<T>(f);
+    }
   }
 }
 
@@ -52,12 +172,17 @@ template <typename T>
 cudaError_t launch(const DropoutArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.x, a.ldx) && vec_ok(a.y, a.ldy) &&
                    (!a.res || vec_ok(a.res, a.ldres));
-  const int64_t chunks = (a.N + 7) / 8;
-  const DropoutParams p = {a.x, a.res, a.y, a.ldx, a.ldres, a.ldy, a.T, a.N, chunks,
+  const int64_t per_row = vec ? a.N / 8 : (a.N + kTile - 1) / kTile;
+  const int64_t units = a.T * per_row;
+  const int unroll = units <= 148 * 8 * 256 ? 1 : DROP_U;
+  const int64_t per_cta = vec ? kThreads * unroll : kThreads / 32;
+  const int64_t ctas = (units + per_cta - 1) / per_cta;
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 2 KB is no GPU's memory
+  const DropoutParams p = {a.x, a.res, a.y, a.ldx, a.ldres, a.ldy, a.T, a.N, units,
+                           Divisor((uint32_t)per_row),
                            {a.drop.seed, a.drop.step, a.drop.threshold, a.drop.scale}};
-  const int64_t ctas = (a.T * chunks + 255) / 256;
-  return launch_pdl(vec ? dropout_kernel<T, true> : dropout_kernel<T, false>,
-                    dim3((unsigned)(ctas < 148 * 8 ? ctas : 148 * 8)), dim3(256), 0, st, p);
+  return launch_pdl(!vec ? dropout_any_kernel<T> : unroll == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, DROP_U>, dim3((unsigned)ctas), dim3(kThreads), 0,
+                    st, p);
 }
 
 }  // namespace

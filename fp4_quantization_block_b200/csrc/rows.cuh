@@ -128,6 +128,51 @@ __device__ __forceinline__ void round8(float (&f)[8]) {
   for (int i = 0; i < 8; ++i) f[i] = to_float(from_float<T>(f[i]));
 }
 
+// ------------------------------------------------------------- division ---
+// Quotients by a divisor d < 2^31 known on the host, for n < 2^31: with s =
+// ceil(log2 d) and m = ceil(2^(32 + s) / d) - 2^32, n / d = (hi(m n) + n) >> s
+// exactly (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", PLDI 1994; the sum stays below 2^32 for these n).
+struct Divisor {
+  uint32_t d, m, s;
+  Divisor() = default;
+  explicit Divisor(uint32_t v) : d(v), m(0), s(0) {
+    while ((uint64_t(1) << s) < v) ++s;
+    m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - v)) / v + 1);
+  }
+  __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
+// ---------------------------------------------------------------- pairs ---
+// A chunk as four packed binary32 pairs, for arithmetic at two values an
+// instruction (fa4_device.cuh): pair i holds columns 2i and 2i + 1.
+__device__ __forceinline__ uint64_t f2_set(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ float f2_lo(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return a;
+}
+__device__ __forceinline__ float f2_hi(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return b;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) { return f2_lo(v) + f2_hi(v); }
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T> &r, uint64_t (&f)[4]) {
+  float v[8];
+  unpack8(r, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void pack8(const uint64_t (&f)[4], Raw8<T> &r) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f[i], v[2 * i], v[2 * i + 1]);
+  pack8(v, r);
+}
+
 // A weight or bias vector: binary32 or the activations' type.
 template <typename T>
 struct Vec {
@@ -176,11 +221,14 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // ----------------------------------------------- rows kept on the chip ---
-// A team of W warps holds one row: warp w's j-th tile is the 256 columns from
-// 256 (j W + w), lane l's chunk the eight from 8 l in it.  Tiles come through
-// a ring of stages in shared memory, private to the warp, filled by
-// asynchronous copies several rows ahead, so that what is in flight does not
-// depend on registers; a warp waits only for its own copies.
+// A team of warps holds one row: a warp has CH tiles of 256 columns each, one
+// after the other; a lane has eight values of a tile as four pairs, for 16-bit
+// types the columns from 8 l, for binary32 four from 4 l and four from 128 +
+// 4 l, so that a warp's 16-byte accesses to memory and to shared memory are
+// consecutive.  Tiles come through a ring of stages in shared memory, private
+// to the warp, filled by asynchronous copies several rows ahead, so that what
+// is in flight does not depend on registers; a warp waits only for its own
+// copies.
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
@@ -203,98 +251,174 @@ __device__ __forceinline__ void cp_async_wait(int n) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 constexpr int kMaxStages = 4;
+constexpr int kTile = 256;
 
-// A warp's copy of columns cb .. cb+255 (those below cols) of a row into a
-// tile.  VEC: 16-byte copies.  Otherwise 4-byte ones where the row allows
-// them (`words`: binary32, or 16-bit rows that start on 4-byte boundaries),
-// and plain loads for 16-bit rows that do not.  Visible to the warp after
-// cp_async_wait and __syncwarp.
+// The tile column of a lane's pair i (its first value).
+template <typename T>
+__device__ __forceinline__ int pair_col(int lane, int i) {
+  return sizeof(T) == 2 ? 8 * lane + 2 * i : (i < 2 ? 0 : 124) + 4 * lane + 2 * i;
+}
+// Dropout of a lane's pairs with the bits of its two half blocks.
+__device__ __forceinline__ void drop_pairs(const Drop &d, const uint32_t (&w)[4], uint64_t (&f)[4]) {
+  const uint32_t t = d.threshold << 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f2_mul(f[i], f2_set(d.scale)), lo, hi);
+    f[i] = f2_pack((w[i] << 16) >= t ? lo : 0.0f, w[i] >= t ? hi : 0.0f);
+  }
+}
+// The bits of a binary32 lane, which has four columns of each of two blocks:
+// of a pair of lanes the even one has the first halves and computed the first
+// block's bits b, the odd one the second halves and the second block's; they
+// exchange the words that the other needs.
+__device__ __forceinline__ void share_bits(const u32x4 &b, int lane, uint32_t (&w)[4]) {
+  const bool odd = lane & 1;
+  const uint32_t g0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? b.x : b.z, 1);
+  const uint32_t g1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? b.y : b.w, 1);
+  w[0] = odd ? g0 : b.x;
+  w[1] = odd ? g1 : b.y;
+  w[2] = odd ? b.z : g0;
+  w[3] = odd ? b.w : g1;
+}
+// Dropout of a lane's values of the tile whose first generator block is
+// `group`.
+template <typename T>
+__device__ __forceinline__ void drop_tile(const Drop &d, uint64_t key, uint32_t row, uint32_t group, int lane,
+                                          uint64_t (&f)[4]) {
+  if (d.threshold == 0u) return;
+  const uint32_t mine = sizeof(T) == 2 ? lane : (lane >> 1) + 16 * (lane & 1);
+  const u32x4 b = philox(group + mine, row, 0u, kDropTag, (uint32_t)key, (uint32_t)(key >> 32));
+  uint32_t w[4] = {b.x, b.y, b.z, b.w};
+  if constexpr (sizeof(T) == 4) share_bits(b, lane, w);
+  drop_pairs(d, w, f);
+}
+
+// A warp's copy of the first `left` of 256 columns from src into a tile.
+// VEC: 16-byte copies.  Otherwise 4-byte ones where the row allows them
+// (`words`: binary32, or 16-bit rows that start on 4-byte boundaries), and
+// plain loads for 16-bit rows that do not.  Visible to the warp after
+// cp_async_wait and __syncwarp.  Columns from `left` on are not touched.
 template <typename T, bool VEC>
-__device__ __forceinline__ void fill_tile(T *tile, const T *row, int cb, int cols, bool words, int lane) {
+__device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool words, int lane) {
   constexpr int kPer16 = 16 / (int)sizeof(T), kPer4 = 4 / (int)sizeof(T);
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < 256 / (32 * kPer16); ++i) {
+    for (int i = 0; i < kTile / (32 * kPer16); ++i) {
       const int e = (32 * i + lane) * kPer16;
-      if (cb + e < cols) cp_async16(tile + e, row + cb + e);
+      if (e < left) cp_async16(tile + e, src + e);
     }
   } else if (sizeof(T) == 4 || words) {
 #pragma unroll
-    for (int i = 0; i < 256 / (32 * kPer4); ++i) {
+    for (int i = 0; i < kTile / (32 * kPer4); ++i) {
       const int e = (32 * i + lane) * kPer4;
-      if (cb + e + kPer4 <= cols)
-        cp_async4(tile + e, row + cb + e);
-      else if (cb + e < cols)
-        tile[e] = row[cb + e];
+      if (e + kPer4 <= left)
+        cp_async4(tile + e, src + e);
+      else if (e < left)
+        tile[e] = src[e];
     }
   } else {
     T v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (cb + 32 * i + lane < cols) v[i] = row[cb + 32 * i + lane];
+      if (32 * i + lane < left) v[i] = src[32 * i + lane];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (cb + 32 * i + lane < cols) tile[32 * i + lane] = v[i];
+      if (32 * i + lane < left) tile[32 * i + lane] = v[i];
   }
 }
-// A lane's chunk of a tile at column c = cb + 8 lane, zeros from cols on.
-template <typename T, bool VEC>
-__device__ __forceinline__ void read_tile(const T *tile, int c, int cols, int lane, float (&f)[8]) {
+// Zeros the columns from `left` on, which no copy touches afterwards: they
+// read as zeros in every row.
+template <typename T>
+__device__ __forceinline__ void clear_tail(T *tile, int left, int lane) {
+  for (int e = (left > 0 ? left : 0) + lane; e < kTile; e += 32) tile[e] = from_float<T>(0.0f);
+}
+// A lane's values of a tile.
+template <typename T>
+__device__ __forceinline__ void read_tile(const T *tile, int lane, uint64_t (&f)[4]) {
   Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4 *>(tile + 8 * lane)[i];
+  r.v[0] = *reinterpret_cast<const uint4 *>(tile + (sizeof(T) == 2 ? 8 : 4) * lane);
+  if constexpr (sizeof(T) == 4) r.v[1] = *reinterpret_cast<const uint4 *>(tile + 128 + 4 * lane);
   unpack8(r, f);
-  if (VEC) {
-    if (c >= cols)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? f[i] : 0.0f;
-  }
 }
-// Stores the warp's 256 columns from cb, lane l holding the eight from 8 l:
-// 16-bit chunks directly, the others through `tile` (which the warp has
-// finished reading), so that neighbouring lanes write neighbouring bytes.
+// Stores the first `left` of the warp's 256 columns at dst.  Rows that allow
+// no 16-byte access go through `tile` (which the warp has finished reading),
+// so that neighbouring lanes write neighbouring elements; the tile's columns
+// from `left` on are not touched.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_tile(T *tile, T *row, int cb, int cols, bool words, int lane,
-                                           const float (&f)[8]) {
-  constexpr int kPer16 = 16 / (int)sizeof(T), kPer4 = 4 / (int)sizeof(T);
+__device__ __forceinline__ void store_tile(T *tile, T *dst, int left, bool words, int lane,
+                                           const uint64_t (&f)[4]) {
   Raw8<T> r;
   pack8(f, r);
-  if constexpr (VEC && sizeof(T) == 2) {
-    if (cb + 8 * lane < cols) *reinterpret_cast<uint4 *>(row + cb + 8 * lane) = r.v[0];
-    return;
-  }
-  __syncwarp();  // the tile's last readers
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(tile + 8 * lane)[i] = r.v[i];
-  __syncwarp();
   if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < 256 / (32 * kPer16); ++i) {
-      const int e = (32 * i + lane) * kPer16;
-      if (cb + e < cols) *reinterpret_cast<uint4 *>(row + cb + e) = *reinterpret_cast<const uint4 *>(tile + e);
-    }
-  } else if (sizeof(T) == 4 || words) {
-#pragma unroll
-    for (int i = 0; i < 256 / (32 * kPer4); ++i) {
-      const int e = (32 * i + lane) * kPer4;
-      if (cb + e + kPer4 <= cols)
-        *reinterpret_cast<uint32_t *>(row + cb + e) = *reinterpret_cast<const uint32_t *>(tile + e);
-      else if (cb + e < cols)
-        row[cb + e] = tile[e];
-    }
+    constexpr int kLane = sizeof(T) == 2 ? 8 : 4;
+    if (kLane * lane < left) *reinterpret_cast<uint4 *>(dst + kLane * lane) = r.v[0];
+    if constexpr (sizeof(T) == 4)
+      if (128 + 4 * lane < left) *reinterpret_cast<uint4 *>(dst + 128 + 4 * lane) = r.v[1];
   } else {
+    __syncwarp();  // the tile's last readers
+    if (pair_col<T>(lane, 3) + 2 <= left) {
+      *reinterpret_cast<uint4 *>(tile + (sizeof(T) == 2 ? 8 : 4) * lane) = r.v[0];
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(tile + 128 + 4 * lane) = r.v[1];
+    } else {
+      float v[8];
+      unpack8(r, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = 32 * i + lane;
-      if (cb + e < cols) row[cb + e] = tile[e];
+      for (int i = 0; i < 8; ++i)
+        if (pair_col<T>(lane, i / 2) + (i & 1) < left)
+          tile[pair_col<T>(lane, i / 2) + (i & 1)] = from_float<T>(v[i]);
+    }
+    __syncwarp();
+    constexpr int kPer4 = 4 / (int)sizeof(T);
+    if (sizeof(T) == 4 || words) {
+#pragma unroll
+      for (int i = 0; i < kTile / (32 * kPer4); ++i) {
+        const int e = (32 * i + lane) * kPer4;
+        if (e + kPer4 <= left)
+          *reinterpret_cast<uint32_t *>(dst + e) = *reinterpret_cast<const uint32_t *>(tile + e);
+        else if (e < left)
+          dst[e] = tile[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = 32 * i + lane;
+        if (e < left) dst[e] = tile[e];
+      }
     }
   }
 }
 
-// Sums of K values over a team of W warps, the same bits in every thread: a
+// Weights in shared memory as a lane reads them: those of binary32 beside
+// 16-bit rows as two planes per tile, the lanes' first four columns and their
+// last four; the others as they lie.
+template <typename T, typename W>
+__device__ __forceinline__ int vec_slot(int c) {
+  if (sizeof(T) == 2 && sizeof(W) == 4)
+    return (c & ~(kTile - 1)) + 128 * ((c >> 2) & 1) + 4 * ((c >> 3) & 31) + (c & 3);
+  return c;
+}
+// The CTA's copy of `cols` weights, zeros up to `room` (complete after
+// cp_async_wait and a barrier).  vec: they start on a 16-byte boundary.
+template <typename T, typename W>
+__device__ __forceinline__ void stage_vec(W *dst, const W *src, int cols, int room, bool vec) {
+  constexpr int kPer16 = 16 / (int)sizeof(W);
+  const int whole = vec ? cols / kPer16 * kPer16 : 0;
+  for (int c = kPer16 * threadIdx.x; c < whole; c += kPer16 * blockDim.x)
+    cp_async16(dst + vec_slot<T, W>(c), src + c);
+  for (int c = whole + threadIdx.x; c < room; c += blockDim.x)
+    dst[vec_slot<T, W>(c)] = c < cols ? src[c] : from_float<W>(0.0f);
+}
+// A lane's staged weights of a tile.
+template <typename T, typename W>
+__device__ __forceinline__ void read_vec(const W *tile, int lane, uint64_t (&f)[4]) {
+  if constexpr (sizeof(T) == sizeof(W) || sizeof(W) == 4) {
+    read_tile<W>(tile, lane, f);
+  } else {  // 16-bit weights beside binary32 rows are not taken
+  }
+}
+
+// Sums of K values over a team of W <= 16 warps, the same bits in every thread: a
 // butterfly in the warp, then over the warps' sums.  `red` holds W x K floats;
 // two uses of one buffer need a barrier of the team between them.
 template <int K>
@@ -306,12 +430,14 @@ __device__ __forceinline__ void team_sum(float (&v)[K], float *red, int W, int w
 #pragma unroll
     for (int k = 0; k < K; ++k) red[warp * K + k] = v[k];
   asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
-  const int pow2 = W > 8 ? (W > 16 ? 32 : 16) : (W > 4 ? 8 : (W > 2 ? 4 : 2)), l = lane & (pow2 - 1);
+  const int l = lane & (W > 8 ? 15 : W > 4 ? 7 : W > 2 ? 3 : 1);
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = l < W ? red[l * K + k] : 0.0f;
-  for (int o = pow2 >> 1; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  for (int o = 8; o > 0; o >>= 1)
+    if (o < W)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
 }
 
 }  // namespace rows

@@ -3,7 +3,12 @@
 //
 // h = silu(g) u, silu(g) = g sg, sg = 1 / (1 + exp(-g)):
 //   du = dh silu(g),   dg = dh u sg (1 + g (1 - sg)),
-// in binary32, each rounded once to bf16.
+// in binary32, each rounded once to bf16.  The reciprocal is the hardware's
+// estimate (one unit in the last place, far inside bf16's step; the quotient
+// of an infinite exponential is the zero that it should be).
+//
+// Bound by memory: 10 bytes per element of h.  A thread has the loads of all
+// its chunks in flight before it computes, and the grid covers dh once.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,38 +21,72 @@ namespace {
 
 using namespace rows;
 
-// One chunk of eight channels of h per thread and step.
-__global__ void __launch_bounds__(256) swiglu_bwd_kernel(const SwigluBwdArgs p) {
+constexpr int kThreads = 256;
+#ifndef SW_U
+#define SW_U 1
+#endif
+constexpr int kUnroll = SW_U;
+
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// dz may be z itself: a thread reads its elements before it writes them.
+__global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArgs p, const int64_t units,
+                                                              const Divisor per_row) {
   using T = __nv_bfloat16;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int64_t chunks = p.F >> 3, total = p.T * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / chunks, c = 8 * (i - r * chunks);
-    const T *z = reinterpret_cast<const T *>(p.z) + r * p.ldz;
-    T *dz = reinterpret_cast<T *>(p.dz) + r * p.lddz;
-    float g[8], u[8], d[8];
-    load8<T, true>(z, c, p.F, g);
-    load8<T, true>(z + p.F, c, p.F, u);
-    load8<T, true>(reinterpret_cast<const T *>(p.dh) + r * p.lddh, c, p.F, d);
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
+  const int64_t row0 = units < (int64_t(1) << 31) ? per_row.quotient((uint32_t)first) : first / per_row.d;
+  const uint32_t unit0 = (uint32_t)(first - row0 * per_row.d);
+  Raw8<T> g[kUnroll], u[kUnroll], d[kUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float e = expf(-g[j]), sg = 1.0f / (1.0f + e);
-      const float du = d[j] * (g[j] * sg);
-      g[j] = d[j] * u[j] * (sg * fmaf(g[j], 1.0f - sg, 1.0f));
-      u[j] = du;
+  for (int k = 0; k < kUnroll; ++k) {
+    const uint32_t n = k * kThreads + threadIdx.x, q = per_row.quotient(unit0 + n);
+    const int64_t row = row0 + q, c = 8 * (int64_t)(unit0 + n - q * per_row.d);
+    if (first + n < units) {
+      const uint16_t *z = p.z + row * p.ldz + c;
+      g[k].v[0] = __ldcs(reinterpret_cast<const uint4 *>(z));
+      u[k].v[0] = __ldcs(reinterpret_cast<const uint4 *>(z + p.F));
+      d[k].v[0] = __ldcs(reinterpret_cast<const uint4 *>(p.dh + row * p.lddh + c));
     }
-    store8<T, true>(dz, c, p.F, g);
-    store8<T, true>(dz + p.F, c, p.F, u);
+  }
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    const uint32_t n = k * kThreads + threadIdx.x, q = per_row.quotient(unit0 + n);
+    const int64_t row = row0 + q, c = 8 * (int64_t)(unit0 + n - q * per_row.d);
+    if (first + n < units) {
+      float gf[8], uf[8], df[8];
+      unpack8(g[k], gf);
+      unpack8(u[k], uf);
+      unpack8(d[k], df);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float sg = reciprocal(1.0f + expf(-gf[j]));
+        const float du = df[j] * (gf[j] * sg);
+        gf[j] = df[j] * uf[j] * (sg * fmaf(gf[j], 1.0f - sg, 1.0f));
+        uf[j] = du;
+      }
+      pack8(gf, g[k]);
+      pack8(uf, u[k]);
+      uint16_t *dz = p.dz + row * p.lddz + c;
+      *reinterpret_cast<uint4 *>(dz) = g[k].v[0];
+      *reinterpret_cast<uint4 *>(dz + p.F) = u[k].v[0];
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu_bwd(const SwigluBwdArgs &a, cudaStream_t st) {
-  const int64_t ctas = (a.T * (a.F >> 3) + 255) / 256;
-  return launch_pdl(swiglu_bwd_kernel, dim3((unsigned)(ctas < 148 * 8 ? ctas : 148 * 8)), dim3(256), 0,
-                    st, a);
+  const int64_t per_row = a.F / 8, units = a.T * per_row;
+  const int64_t ctas = (units + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 8 KB is no GPU's memory
+  return launch_pdl(swiglu_bwd_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, st, a, units,
+                    Divisor((uint32_t)per_row));
 }
 
 }  // namespace fa4
