@@ -20,7 +20,7 @@ namespace {
 using namespace rows;
 
 #ifndef DROP_U
-#define DROP_U 2
+#define DROP_U 4
 #endif
 constexpr int kThreads = 256;
 
@@ -28,7 +28,7 @@ struct DropoutParams {
   const void *x, *res;
   void *y;
   int64_t ldx, ldres, ldy, T, N;
-  int64_t units;  // of the matrix: chunks of eight columns, or warps' tiles
+  int64_t units;  // of the matrix: chunks of eight columns of a group of rows, or warps' tiles
   Divisor per_row;
   Drop drop;
 };
@@ -42,60 +42,72 @@ __device__ __forceinline__ void place(const DropoutParams &p, int64_t row0, uint
   unit = u - q * p.per_row.d;
 }
 
-// Rows on 16-byte boundaries, N a multiple of eight.  A warp step is 32
-// consecutive chunks; a lane of a 16-bit type has one of them, a lane of
-// binary32 the even or odd halves of two (16-byte accesses that are
-// consecutive over the lanes).  y may be x or res itself: a thread reads its
+// Rows on 16-byte boundaries, N a multiple of eight.  A thread takes the same
+// chunk of ROWS consecutive rows (one division, one key schedule and the first
+// half of the generator's first round for all of them); a unit is a chunk of
+// such a group of rows.  Consecutive lanes have consecutive units; binary32
+// lanes have the even or odd halves of two of them, so that their 16-byte
+// accesses are consecutive.  y may be x or res itself: a thread reads its
 // elements before it writes them.
-template <typename T, int kUnroll>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p) {
-  constexpr int H = sizeof(T) / 2;  // 16-byte pieces of a lane
+  constexpr int H = sizeof(T) / 2;  // 16-byte pieces of a lane in a row
   constexpr int kPer16 = 16 / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
   const uint64_t key = p.drop.key();
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
-  const int64_t row0 = p.units < (int64_t(1) << 31) ? p.per_row.quotient((uint32_t)first) : first / p.per_row.d;
-  const uint32_t unit0 = (uint32_t)(first - row0 * p.per_row.d);
-  uint4 x[kUnroll][H], r[kUnroll][H];
-  // the chunk of the CTA's that a lane's h-th piece of step k lies in
-  auto chunk = [&](int k, int h) {
-    const uint32_t warp0 = k * kThreads + (threadIdx.x & ~31u);
-    return H == 1 ? warp0 + lane : warp0 + 16 * h + (lane >> 1);
-  };
+  const int64_t first = (int64_t)blockIdx.x * kThreads;
+  const int64_t group0 = p.units < (int64_t(1) << 31) ? p.per_row.quotient((uint32_t)first) : first / p.per_row.d;
+  const uint32_t unit0 = (uint32_t)(first - group0 * p.per_row.d);
+  const uint32_t warp0 = threadIdx.x & ~31u;
+  int64_t row[H];
+  uint32_t unit[H], c[H];
+  bool in[H];
 #pragma unroll
-  for (int k = 0; k < kUnroll; ++k)
+  for (int h = 0; h < H; ++h) {
+    const uint32_t k = H == 1 ? threadIdx.x : warp0 + 16 * h + (lane >> 1);
+    place(p, group0, unit0, k, row[h], unit[h]);
+    row[h] *= ROWS;
+    c[h] = 8 * unit[h] + (H == 2 ? kPer16 * (lane & 1) : 0);
+    in[h] = first + k < p.units;
+  }
+  uint4 x[ROWS][H], r[ROWS][H];
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (first + chunk(k, h) < p.units) {
-        int64_t row;
-        uint32_t unit;
-        place(p, row0, unit0, chunk(k, h), row, unit);
-        const int64_t c = 8 * (int64_t)unit + (H == 2 ? kPer16 * (lane & 1) : 0);
-        x[k][h] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.x) + row * p.ldx + c));
-        if (p.res)
-          r[k][h] = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.res) + row * p.ldres + c));
+  for (int h = 0; h < H; ++h) {
+    const T *px = static_cast<const T *>(p.x) + row[h] * p.ldx + c[h];
+    const T *pr = static_cast<const T *>(p.res) + row[h] * p.ldres + c[h];
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+      if (in[h] && (ROWS == 1 || row[h] + k < p.T)) {
+        x[k][h] = __ldcs(reinterpret_cast<const uint4 *>(px));
+        if (p.res) r[k][h] = __ldcs(reinterpret_cast<const uint4 *>(pr));
       }
-#pragma unroll
-  for (int k = 0; k < kUnroll; ++k) {
-    // the block whose bits this lane computes: its chunk, or (binary32) the
-    // first or the second of the two that it shares with its neighbour
-    int64_t row;
-    uint32_t unit;
-    place(p, row0, unit0, chunk(k, H == 1 ? 0 : lane & 1), row, unit);
-    uint32_t w[4];
-    if (p.drop.threshold) {
-      const u32x4 b = philox(unit, (uint32_t)row, 0u, kDropTag, (uint32_t)key, (uint32_t)(key >> 32));
-      w[0] = b.x, w[1] = b.y, w[2] = b.z, w[3] = b.w;
-      if constexpr (H == 2) share_bits(b, lane, w);
+      px += p.ldx;
+      pr += p.ldres;
     }
+  }
+  // the block whose bits this lane computes: its chunk, or (binary32) the
+  // first or the second of the two that it shares with its neighbour
+  const int mine = H == 1 ? 0 : lane & 1;
+  const uint32_t block = mine ? unit[H - 1] : unit[0];
+  const int64_t brow = mine ? row[H - 1] : row[0];
+  T *py[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) py[h] = static_cast<T *>(p.y) + row[h] * p.ldy + c[h];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
     Raw8<T> raw;
     uint64_t f[4];
 #pragma unroll
     for (int h = 0; h < H; ++h) raw.v[h] = x[k][h];
     unpack8(raw, f);
-    if (p.drop.threshold) drop_pairs(p.drop, w, f);
+    if (p.drop.threshold) {
+      const u32x4 b = philox(block, (uint32_t)brow + k, 0u, kDropTag, (uint32_t)key, (uint32_t)(key >> 32));
+      uint32_t w[4] = {b.x, b.y, b.z, b.w};
+      if constexpr (H == 2) share_bits(b, lane, w);
+      drop_pairs(p.drop, w, f);
+    }
     if (p.res) {
       uint64_t g[4];
 #pragma unroll
@@ -106,12 +118,10 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
     }
     pack8(f, raw);
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-      if (first + chunk(k, h) < p.units) {
-        place(p, row0, unit0, chunk(k, h), row, unit);
-        const int64_t c = 8 * (int64_t)unit + (H == 2 ? kPer16 * (lane & 1) : 0);
-        *reinterpret_cast<uint4 *>(static_cast<T *>(p.y) + row * p.ldy + c) = raw.v[h];
-      }
+    for (int h = 0; h < H; ++h) {
+      if (in[h] && (ROWS == 1 || row[h] + k < p.T)) *reinterpret_cast<uint4 *>(py[h]) = raw.v[h];
+      py[h] += p.ldy;
+    }
   }
 }
 
@@ -173,16 +183,15 @@ cudaError_t launch(const DropoutArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.x, a.ldx) && vec_ok(a.y, a.ldy) &&
                    (!a.res || vec_ok(a.res, a.ldres));
   const int64_t per_row = vec ? a.N / 8 : (a.N + kTile - 1) / kTile;
-  const int64_t units = a.T * per_row;
-  const int unroll = units <= 148 * 8 * 256 ? 1 : DROP_U;
-  const int64_t per_cta = vec ? kThreads * unroll : kThreads / 32;
+  const int rows = vec && a.T * per_row > 148 * 8 * kThreads ? DROP_U : 1;
+  const int64_t per_cta = vec ? kThreads : kThreads / 32, units = (a.T + rows - 1) / rows * per_row;
   const int64_t ctas = (units + per_cta - 1) / per_cta;
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 2 KB is no GPU's memory
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 4 KB is no GPU's memory
   const DropoutParams p = {a.x, a.res, a.y, a.ldx, a.ldres, a.ldy, a.T, a.N, units,
                            Divisor((uint32_t)per_row),
                            {a.drop.seed, a.drop.step, a.drop.threshold, a.drop.scale}};
-  return launch_pdl(!vec ? dropout_any_kernel<T> : unroll == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, DROP_U>, dim3((unsigned)ctas), dim3(kThreads), 0,
-                    st, p);
+  return launch_pdl(!vec ? dropout_any_kernel<T> : rows == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, DROP_U>,
+                    dim3((unsigned)ctas), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace

@@ -235,6 +235,11 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
+// Only the first `bytes` are read; the rest of the 16 are zeros.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -294,98 +299,125 @@ __device__ __forceinline__ void drop_tile(const Drop &d, uint64_t key, uint32_t 
   drop_pairs(d, w, f);
 }
 
-// A warp's copy of the first `left` of 256 columns from src into a tile.
-// VEC: 16-byte copies.  Otherwise 4-byte ones where the row allows them
-// (`words`: binary32, or 16-bit rows that start on 4-byte boundaries), and
-// plain loads for 16-bit rows that do not.  Visible to the warp after
-// cp_async_wait and __syncwarp.  Columns from `left` on are not touched.
+// A tile of a ring.  VEC: rows on 16-byte boundaries.  Otherwise a row starts
+// `mis` bytes past one, and the tile holds the aligned 16-byte words that the
+// columns lie in, one word more.
 template <typename T, bool VEC>
-__device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool words, int lane) {
-  constexpr int kPer16 = 16 / (int)sizeof(T), kPer4 = 4 / (int)sizeof(T);
+constexpr int kTileLen = VEC ? kTile : kTile + 16 / (int)sizeof(T);
+__device__ __forceinline__ int misaligned(const void *p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15u); }
+
+// A warp's copy of the first `left` of 256 columns from src into a tile, zeros
+// after them (VEC: what lies after them is not touched).  Visible to the warp
+// after cp_async_wait and __syncwarp.  Unless VEC the first word may begin
+// before src, in the row before or its padding; `head` says that there is no
+// such row, and the word is copied by elements.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool head, int lane) {
+  constexpr int kPer16 = 16 / (int)sizeof(T), kWords = kTile / kPer16;
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kTile / (32 * kPer16); ++i) {
+    for (int i = 0; i < kWords / 32; ++i) {
       const int e = (32 * i + lane) * kPer16;
       if (e < left) cp_async16(tile + e, src + e);
     }
-  } else if (sizeof(T) == 4 || words) {
-#pragma unroll
-    for (int i = 0; i < kTile / (32 * kPer4); ++i) {
-      const int e = (32 * i + lane) * kPer4;
-      if (e + kPer4 <= left)
-        cp_async4(tile + e, src + e);
-      else if (e < left)
-        tile[e] = src[e];
-    }
   } else {
-    T v[8];
+    const int mis = misaligned(src), total = (left < kTile ? left : kTile) * (int)sizeof(T) + mis;
+    const char *word0 = reinterpret_cast<const char *>(src) - mis;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (32 * i + lane < left) v[i] = src[32 * i + lane];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (32 * i + lane < left) tile[32 * i + lane] = v[i];
+    for (int i = 0; i < kWords + 1; i += 32) {
+      const int w = i + lane;
+      if (w > kWords) break;
+      const int bytes = total - 16 * w;
+      if (w == 0 && head && mis) {
+        const int off = mis / (int)sizeof(T);
+        for (int e = 0; e < kPer16 - off; ++e) tile[off + e] = e < left ? src[e] : from_float<T>(0.0f);
+      } else {
+        cp_async16(tile + w * kPer16, bytes > 0 ? word0 + 16 * w : reinterpret_cast<const char *>(src),
+                   bytes < 0 ? 0 : bytes > 16 ? 16 : bytes);
+      }
+    }
   }
 }
-// Zeros the columns from `left` on, which no copy touches afterwards: they
-// read as zeros in every row.
+// Zeros a tile of `len` elements from `left` on, which no copy touches
+// afterwards: those columns read as zeros in every row.
 template <typename T>
-__device__ __forceinline__ void clear_tail(T *tile, int left, int lane) {
-  for (int e = (left > 0 ? left : 0) + lane; e < kTile; e += 32) tile[e] = from_float<T>(0.0f);
+__device__ __forceinline__ void clear_tail(T *tile, int left, int len, int lane) {
+  for (int e = (left > 0 ? left : 0) + lane; e < len; e += 32) tile[e] = from_float<T>(0.0f);
 }
-// A lane's values of a tile.
-template <typename T>
-__device__ __forceinline__ void read_tile(const T *tile, int lane, uint64_t (&f)[4]) {
+// The 16 bytes that start `mis` (even, the same in the whole warp) bytes into
+// two neighbouring words.
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int mis) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (mis & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (mis & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (mis & 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A lane's values of a tile (mis: of the row's start, unless VEC).
+template <typename T, bool VEC>
+__device__ __forceinline__ void read_tile(const T *tile, int mis, int lane, uint64_t (&f)[4]) {
+  constexpr int kLane = sizeof(T) == 2 ? 8 : 4;
   Raw8<T> r;
-  r.v[0] = *reinterpret_cast<const uint4 *>(tile + (sizeof(T) == 2 ? 8 : 4) * lane);
-  if constexpr (sizeof(T) == 4) r.v[1] = *reinterpret_cast<const uint4 *>(tile + 128 + 4 * lane);
+#pragma unroll
+  for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+    const uint4 *w = reinterpret_cast<const uint4 *>(tile + 128 * h + kLane * lane);
+    r.v[h] = VEC ? w[0] : shifted(w[0], w[1], mis);
+  }
   unpack8(r, f);
 }
-// Stores the first `left` of the warp's 256 columns at dst.  Rows that allow
-// no 16-byte access go through `tile` (which the warp has finished reading),
-// so that neighbouring lanes write neighbouring elements; the tile's columns
-// from `left` on are not touched.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store_tile(T *tile, T *dst, int left, bool words, int lane,
-                                           const uint64_t (&f)[4]) {
-  Raw8<T> r;
-  pack8(f, r);
+// Stores the first `left` of the warp's CH x 256 columns at dst.  VEC: each
+// lane its 16-byte words.  Otherwise through `stage` (CH tiles that the warp
+// has finished reading): the columns in order, then the aligned words of dst
+// out of them, and the elements before the first and after the last of these.
+template <typename T, int CH, bool VEC>
+__device__ __forceinline__ void store_tiles(T *stage, T *dst, int left, int lane, const uint64_t (&f)[CH][4]) {
+  constexpr int kLane = sizeof(T) == 2 ? 8 : 4, P = 16 / (int)sizeof(T);
   if constexpr (VEC) {
-    constexpr int kLane = sizeof(T) == 2 ? 8 : 4;
-    if (kLane * lane < left) *reinterpret_cast<uint4 *>(dst + kLane * lane) = r.v[0];
-    if constexpr (sizeof(T) == 4)
-      if (128 + 4 * lane < left) *reinterpret_cast<uint4 *>(dst + 128 + 4 * lane) = r.v[1];
-  } else {
-    __syncwarp();  // the tile's last readers
-    if (pair_col<T>(lane, 3) + 2 <= left) {
-      *reinterpret_cast<uint4 *>(tile + (sizeof(T) == 2 ? 8 : 4) * lane) = r.v[0];
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(tile + 128 + 4 * lane) = r.v[1];
-    } else {
-      float v[8];
-      unpack8(r, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (pair_col<T>(lane, i / 2) + (i & 1) < left)
-          tile[pair_col<T>(lane, i / 2) + (i & 1)] = from_float<T>(v[i]);
+    for (int j = 0; j < CH; ++j) {
+      Raw8<T> r;
+      pack8(f[j], r);
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+        const int c = j * kTile + 128 * h + kLane * lane;
+        if (c < left) *reinterpret_cast<uint4 *>(dst + c) = r.v[h];
+      }
+    }
+  } else {
+    __syncwarp();  // the stage's last readers
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      Raw8<T> r;
+      pack8(f[j], r);
+#pragma unroll
+      for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+        *reinterpret_cast<uint4 *>(stage + j * kTile + 128 * h + kLane * lane) = r.v[h];
     }
     __syncwarp();
-    constexpr int kPer4 = 4 / (int)sizeof(T);
-    if (sizeof(T) == 4 || words) {
+    const int n = left < CH * kTile ? left : CH * kTile;
+    const int mis = misaligned(dst), off = mis / (int)sizeof(T);
+    // word k of dst's has the columns from k P - off
 #pragma unroll
-      for (int i = 0; i < kTile / (32 * kPer4); ++i) {
-        const int e = (32 * i + lane) * kPer4;
-        if (e + kPer4 <= left)
-          *reinterpret_cast<uint32_t *>(dst + e) = *reinterpret_cast<const uint32_t *>(tile + e);
-        else if (e < left)
-          dst[e] = tile[e];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = 32 * i + lane;
-        if (e < left) dst[e] = tile[e];
+    for (int i = 0; i <= CH * kTile / P; i += 32) {
+      const int k = i + lane, c = k * P - off;
+      if (c >= 0 && c + P <= n) {
+        const uint4 *w = reinterpret_cast<const uint4 *>(stage) + k;
+        *reinterpret_cast<uint4 *>(dst + c) = mis ? shifted(w[-1], w[0], 16 - mis) : w[0];
       }
     }
+    const int head = !mis ? 0 : P - off < n ? P - off : n;
+    const int last = (n + off) / P * P - off, tail = last > head ? last : head;
+    const int c = lane < 16 ? lane : tail + lane - 16;
+    if (lane < 16 ? c < head : c < n) dst[c] = stage[c];
   }
 }
 
@@ -413,31 +445,25 @@ __device__ __forceinline__ void stage_vec(W *dst, const W *src, int cols, int ro
 template <typename T, typename W>
 __device__ __forceinline__ void read_vec(const W *tile, int lane, uint64_t (&f)[4]) {
   if constexpr (sizeof(T) == sizeof(W) || sizeof(W) == 4) {
-    read_tile<W>(tile, lane, f);
+    read_tile<W, true>(tile, 0, lane, f);
   } else {  // 16-bit weights beside binary32 rows are not taken
   }
 }
 
-// Sums of K values over a team of W <= 16 warps, the same bits in every thread: a
-// butterfly in the warp, then over the warps' sums.  `red` holds W x K floats;
-// two uses of one buffer need a barrier of the team between them.
-template <int K>
-__device__ __forceinline__ void team_sum(float (&v)[K], float *red, int W, int warp, int lane, int bar) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  if (W == 1) return;
-  if (lane == 0)
-#pragma unroll
-    for (int k = 0; k < K; ++k) red[warp * K + k] = v[k];
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * W) : "memory");
-  const int l = lane & (W > 8 ? 15 : W > 4 ? 7 : W > 2 ? 3 : 1);
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = l < W ? red[l * K + k] : 0.0f;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1)
-    if (o < W)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+// ------------------------------------------------------------- clusters ---
+// Writes v to the same place of the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ void cluster_store(float2 *place, int rank, float2 v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(place)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+}
+// The two halves of a barrier of all threads of a cluster (of the CTA where
+// there is none): what was written before the arrival is seen after the wait.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace rows
