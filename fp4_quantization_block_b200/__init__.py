@@ -16,6 +16,7 @@ Hadamard of its section "Two Key Numerical Techniques".
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -147,8 +148,6 @@ def _on_tensor_device(fn):
     QTensor's payload counts) current: the library picks the device's SM
     count and scratch from the current device, and launches on that
     device's current stream."""
-    import functools
-
     @functools.wraps(fn)
     def wrapped(*args, **kwargs):
         for a in (*args, *kwargs.values()):
@@ -594,12 +593,26 @@ def gemm_mxout(A: QTensor, B: QTensor, alpha: float = 1.0, store_d: bool = True,
 DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
+def _on_first_device(fn):
+    """_on_tensor_device for the calls whose first argument is a matrix: small
+    calls of theirs cost what their checks cost."""
+    @functools.wraps(fn)
+    def wrapped(*args, **kwargs):
+        x = args[0] if args else next(iter(kwargs.values()), None)
+        if isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
+    return wrapped
+
+
 def _rows(x: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
     """The leading dimension of a 2-D CUDA matrix of one of the DTYPEs (with
     `like`: of its shape, type and device)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda or x.dtype not in DTYPE:
         raise ValueError(f"{name} must be a 2-D bf16, fp16 or fp32 CUDA tensor")
-    if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
+    if like is not None and (x.shape != like.shape or x.dtype is not like.dtype or
+                             x.get_device() != like.get_device()):
         raise ValueError(f"{name} must be a {list(like.shape)} {like.dtype} tensor on {like.device}")
     rows, cols = x.shape
     ld, unit = x.stride()
@@ -612,8 +625,13 @@ def _rows(x: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
     return ld
 
 
-def _new_rows(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty_like(x, memory_format=torch.contiguous_format)
+def _out_rows(out: torch.Tensor | None, name: str, like: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """The caller's output or a new contiguous one, and its leading dimension."""
+    if out is not None:
+        return out, _rows(out, name, like)
+    rows, cols = like.shape
+    return (torch.empty_like(like, memory_format=torch.contiguous_format),
+            cols if rows > 1 else -(-cols // 8) * 8)
 
 
 def _new_f32(x: torch.Tensor, n: int) -> torch.Tensor:
@@ -621,30 +639,39 @@ def _new_f32(x: torch.Tensor, n: int) -> torch.Tensor:
 
 
 def _vector(v: torch.Tensor, n: int, dtypes: tuple, device, name: str):
-    if not isinstance(v, torch.Tensor) or v.dtype not in dtypes or v.shape != (n,) or \
+    if not isinstance(v, torch.Tensor) or v.dim() != 1 or v.numel() != n or v.dtype not in dtypes or \
             v.device != device or not v.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor of "
                          f"{' or '.join(str(d) for d in dtypes)} on {device}")
 
 
 def _weights(weight, bias, x) -> int:
-    _vector(weight, x.shape[1], (x.dtype, torch.float32), x.device, "weight")
+    n, dev = x.shape[1], x.device
+    _vector(weight, n, (x.dtype, torch.float32), dev, "weight")
     if bias is not None:
-        _vector(bias, x.shape[1], (weight.dtype,), x.device, "bias")
+        _vector(bias, n, (weight.dtype,), dev, "bias")
     return DTYPE[weight.dtype]
 
 
+def _new_stats(x, center):
+    rstd = _new_f32(x, x.shape[0])
+    return torch.empty_like(rstd) if center else None, rstd
+
+
 def _stats(mean, rstd, center, x):
-    _vector(rstd, x.shape[0], (torch.float32,), x.device, "rstd")
+    n, dev = x.shape[0], x.device
+    _vector(rstd, n, (torch.float32,), dev, "rstd")
     if center:
-        _vector(mean, x.shape[0], (torch.float32,), x.device, "mean")
+        _vector(mean, n, (torch.float32,), dev, "mean")
 
 
 def _step(step, x):
-    if step is not None and (not isinstance(step, torch.Tensor) or step.dtype != torch.int64 or
-                             step.numel() != 1 or step.device != x.device):
+    if step is None:
+        return None
+    if not isinstance(step, torch.Tensor) or step.dtype != torch.int64 or step.numel() != 1 or \
+            step.device != x.device:
         raise ValueError(f"step must be a tensor of one int64 on {x.device}")
-    return _ptr(step)
+    return step.data_ptr()
 
 
 def _grads(dweight, dbias, bias_grad, x):
@@ -656,13 +683,15 @@ def _grads(dweight, dbias, bias_grad, x):
     if not bias_grad:
         return dweight, None
     if dbias is None:
-        dbias = _new_f32(x, n)
+        dbias = torch.empty_like(dweight)
     else:
         _vector(dbias, n, (torch.float32,), dev, "dbias")
     return dweight, dbias
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_ws_bytes(rows: int, cols: int) -> int:
+    """Bytes of workspace of the layer norms' backward calls."""
     n = ctypes.c_size_t()
     _check(lib().fa4_layernorm_ws_bytes(rows, cols, ctypes.byref(n)), "fa4_layernorm_ws_bytes")
     return n.value
@@ -676,7 +705,7 @@ def _norm_ws(ws, x):
     return ws
 
 
-@_on_tensor_device
+@_on_first_device
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
                    eps: float = 1e-5, center: bool = True, out: torch.Tensor | None = None
                    ) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor]:
@@ -686,17 +715,16 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     out may be x."""
     ldx = _rows(x, "x")
     wd = _weights(weight, bias, x)
-    y = _new_rows(x) if out is None else out
-    ldy = _rows(y, "out", x)
+    y, ldy = _out_rows(out, "out", x)
     T, N = x.shape
-    mean, rstd = _new_f32(x, T) if center else None, _new_f32(x, T)
+    mean, rstd = _new_stats(x, center)
     _check(lib().fa4_layernorm_fwd(_ptr(x), ldx, T, N, DTYPE[x.dtype], _ptr(weight), _ptr(bias), wd,
                                    eps, 1 if center else 0, _ptr(y), ldy, _ptr(mean), _ptr(rstd),
                                    _stream(x.device)), "fa4_layernorm_fwd")
     return y, mean, rstd
 
 
-@_on_tensor_device
+@_on_first_device
 def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                    mean: torch.Tensor | None, rstd: torch.Tensor, center: bool = True,
                    bias_grad: bool = True, dres: torch.Tensor | None = None,
@@ -711,8 +739,7 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     wd = _weights(weight, None, x)
     _stats(mean, rstd, center, x)
     ldr = 0 if dres is None else _rows(dres, "dres", x)
-    dx = _new_rows(x) if dx is None else dx
-    lddx = _rows(dx, "dx", x)
+    dx, lddx = _out_rows(dx, "dx", x)
     dweight, dbias = _grads(dweight, dbias, bias_grad, x)
     ws = _norm_ws(ws, x)
     T, N = x.shape
@@ -724,7 +751,7 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     return dx, dweight, dbias
 
 
-@_on_tensor_device
+@_on_first_device
 def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None
                 ) -> torch.Tensor:
@@ -735,29 +762,27 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None 
     residual."""
     ldx = _rows(x, "x")
     ldr = 0 if residual is None else _rows(residual, "residual", x)
-    y = _new_rows(x) if out is None else out
-    ldy = _rows(y, "out", x)
+    y, ldy = _out_rows(out, "out", x)
     _check(lib().fa4_dropout_fwd(_ptr(x), ldx, _ptr(residual), ldr, x.shape[0], x.shape[1],
                                  DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF, _step(step, x),
                                  _ptr(y), ldy, _stream(x.device)), "fa4_dropout_fwd")
     return y
 
 
-@_on_tensor_device
+@_on_first_device
 def dropout_bwd(dy: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """dx of dropout_fwd under the same p, seed and step (the residual's
     gradient is dy itself).  out may be dy."""
     lddy = _rows(dy, "dy")
-    dx = _new_rows(dy) if out is None else out
-    lddx = _rows(dx, "out", dy)
+    dx, lddx = _out_rows(out, "out", dy)
     _check(lib().fa4_dropout_bwd(_ptr(dy), lddy, dy.shape[0], dy.shape[1], DTYPE[dy.dtype], p,
                                  seed & 0xFFFFFFFFFFFFFFFF, _step(step, dy), _ptr(dx), lddx,
                                  _stream(dy.device)), "fa4_dropout_bwd")
     return dx
 
 
-@_on_tensor_device
+@_on_first_device
 def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
                                bias: torch.Tensor | None, p: float, seed: int,
                                step: torch.Tensor | None = None, eps: float = 1e-5,
@@ -769,11 +794,9 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
     residual and out may be x."""
     ldx, ldr = _rows(x, "x"), _rows(residual, "residual", x)
     wd = _weights(weight, bias, x)
-    y = _new_rows(x) if out is None else out
-    s = _new_rows(x) if s is None else s
-    ldy, lds = _rows(y, "out", x), _rows(s, "s", x)
+    (y, ldy), (s, lds) = _out_rows(out, "out", x), _out_rows(s, "s", x)
     T, N = x.shape
-    mean, rstd = _new_f32(x, T) if center else None, _new_f32(x, T)
+    mean, rstd = _new_stats(x, center)
     _check(lib().fa4_dropout_add_layernorm_fwd(
         _ptr(x), ldx, _ptr(residual), ldr, T, N, DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF,
         _step(step, x), _ptr(weight), _ptr(bias), wd, eps, 1 if center else 0, _ptr(s), lds, _ptr(y),
@@ -781,7 +804,7 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
     return y, s, mean, rstd
 
 
-@_on_tensor_device
+@_on_first_device
 def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: torch.Tensor,
                                weight: torch.Tensor, mean: torch.Tensor | None, rstd: torch.Tensor,
                                p: float, seed: int, step: torch.Tensor | None = None,
@@ -798,9 +821,7 @@ def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: tor
     ldds = 0 if ds is None else _rows(ds, "ds", s)
     wd = _weights(weight, None, s)
     _stats(mean, rstd, center, s)
-    dx = _new_rows(s) if dx is None else dx
-    dres = _new_rows(s) if dres is None else dres
-    lddx, lddr = _rows(dx, "dx", s), _rows(dres, "dres", s)
+    (dx, lddx), (dres, lddr) = _out_rows(dx, "dx", s), _out_rows(dres, "dres", s)
     dweight, dbias = _grads(dweight, dbias, bias_grad, s)
     ws = _norm_ws(ws, s)
     T, N = s.shape
@@ -812,7 +833,7 @@ def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: tor
     return dx, dres, dweight, dbias
 
 
-@_on_tensor_device
+@_on_first_device
 def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """dz[T, 2F] of the SwiGLU producer (swiglu_quantize) from the gradient
     dh[T, F] of h: the dY that linear_bwd of the gate+up linear takes.  out
@@ -822,7 +843,7 @@ def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = Non
     if F2 % 2 or dh.shape != (T, F2 // 2) or dh.device != z.device:
         raise ValueError(f"z must hold gate and up halves and dh must be [{T}, {F2 // 2}] on {z.device}")
     if out is None:
-        out = _new_rows(z)
+        out = torch.empty_like(z, memory_format=torch.contiguous_format)
     else:
         _check_out(out, (T, F2), (torch.bfloat16,), z.device, "out", row_stride=True)
     _check(lib().fa4_swiglu_bwd(_ptr(z), ldz, _ptr(dh), lddh, T, F2 // 2, _ptr(out), out.stride(0),

@@ -31,9 +31,13 @@ __global__ void __launch_bounds__(kSumThreads)
 
 }  // namespace
 
+// As many partial sums as there can be clusters at once (launch_bwd), or row
+// groups where rows are too long for a cluster; never more than rows.
 int norm_partials_count(int64_t T, int64_t N) {
-  const int w = norm::wide_splits(T, N);
-  return w > norm::kSms ? w : norm::kSms;
+  int n = norm::wide_splits(T, N);
+  for (int log = 3; log >= 0; --log)
+    if (N <= (int64_t)norm::kBwdRow << log) n = norm::kMaxClusters[log];
+  return T < n ? (int)T : n;
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs &a, cudaStream_t st) {

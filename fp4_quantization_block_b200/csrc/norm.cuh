@@ -53,6 +53,8 @@ struct Layout {
 constexpr int kSms = 148;
 constexpr int kMaxClusters[4] = {148, 74, 33, 15};  // of 1, 2, 4 and 8 CTAs that run at once, one per SM
 constexpr size_t kMaxSmem = 224 * 1024;  // the static arrays' share left out
+constexpr int kBwdWarps = 16;                // of a CTA of the backward pass
+constexpr int kBwdRow = kBwdWarps * 2 * kTile;  // the columns that it holds at most
 constexpr int kWideThreads = 512;
 
 // Sum over the CTA's threads, the same bits in each of them.

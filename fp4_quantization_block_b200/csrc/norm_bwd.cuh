@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(const BwdParams p) {
 // too wide for a CTA are shared by a cluster of CTAs, each with some of the
 // columns (and fewer partial sums to write): every warp sends its part of the
 // two sums to all of them.
-constexpr int kBwdWarps = 16;
 template <typename T, typename W, int CH, bool VEC, bool FUSED, bool DS, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdParams p, const Layout g) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -130,6 +129,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   W *const wsm = reinterpret_cast<W *>(smem + (size_t)g.warps * g.teams * g.stages * kStage * sizeof(T));
   const uint32_t q = cid * g.teams + team;
   const int n = g.rows(q);
+  // (backward reads whole rooms: a tile past the row's end is zeros for good)
 #pragma unroll
   for (int j = 0; j < CH; ++j)
     if (left - j * kTile < (VEC ? kTile : 1))
@@ -335,9 +335,17 @@ cudaError_t launch_bwd(BwdParams p, int *n, cudaStream_t st) {
   const int ch = p.N <= 256 ? 1 : 2, warps = ceil_div(p.N < (1 << 17) ? p.N : (1 << 17), kTile * ch);
   Layout g = {};
   g.wvec = vec_ok(p.w, 8);
-  g.cluster = 1;
+  // As few CTAs to a row as its columns need; but where a cluster of eight
+  // takes all rows in two rounds, that one cluster, which needs no partial sums
+  // and no second launch (8 x 4096 bf16: 3.3 us against 5.8; at four rounds
+  // the second launch is cheaper: 64 x 4096 6.8 us against 9.7).
   int log = 0;
-  while (g.cluster < 8 && ceil_div(warps, g.cluster) > kBwdWarps) g.cluster *= 2, ++log;
+  while (log < 3 && ceil_div(warps, 1 << log) > kBwdWarps) ++log;
+  const int eighth = ceil_div(warps, 8), at_once = eighth <= kBwdWarps ? kBwdWarps / eighth : 0;
+  const bool few = ch == 2 && p.T <= 2 * at_once;
+  if (few)
+    while (log < 3 && (1 << log) < warps) ++log;
+  g.cluster = 1 << log;
   g.warps = ceil_div(warps, g.cluster);
   const size_t vecs = (size_t)g.warps * ch * kTile * sizeof(W);
   // rows at a time as if ds were there, so that dw and db do not depend on it
@@ -351,7 +359,7 @@ cudaError_t launch_bwd(BwdParams p, int *n, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_pdl(norm_dx_wide_kernel<T, VEC, FUSED>, dim3(row_ctas(p.T)), dim3(kWideThreads), 0, st, p);
   }
-  const int most = kMaxClusters[log];
+  const int most = few ? 1 : kMaxClusters[log];
   g.teams = kBwdWarps / g.warps;
   if (g.warps > 1 && g.teams > 15) g.teams = 15;  // named barriers
   while (g.teams > 1 && (vecs + 3 * g.teams * most_team > kMaxSmem || p.T <= (int64_t)most * (g.teams - 1)))

@@ -106,12 +106,14 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
   float2 *red0 = &red[0][team * g.warps], *red1 = &red[1][team * g.warps];
   const uint32_t q = blockIdx.x * g.teams + team;
   const int n = g.rows(q);
+  if constexpr (VEC) {
 #pragma unroll
-  for (int j = 0; j < CH; ++j)
-    if (left - j * kTile < (VEC ? kTile : 1))
-      for (int s = 0; s < A * g.stages; ++s)
-        clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
-  __syncwarp();
+    for (int j = 0; j < CH; ++j)
+      if (left - j * kTile > 0 && left - j * kTile < kTile)
+        for (int s = 0; s < A * g.stages; ++s)
+          clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
+    __syncwarp();
+  }
   grid_dependency_wait();
   grid_dependents_launch();
   stage_vec<T, W>(wsm, static_cast<const W *>(p.w), (int)p.N, room, g.wvec);
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
       const bool head = !VEC && q == 0 && col == 0 && ahead == n;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        if (!VEC && left - j * kTile <= 0) continue;
+        if (left - j * kTile <= 0) break;
         fill_tile<T, VEC>(ft + j * kLen, fx + j * kTile, left - j * kTile, head && j == 0, lane);
         if constexpr (FUSED)
           fill_tile<T, VEC>(ft + (CH + j) * kLen, fr + j * kTile, left - j * kTile, head && j == 0, lane);
@@ -165,6 +167,10 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
     uint64_t v[CH][4], acc = 0ull;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
+      if (left - j * kTile <= 0) {
+        v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0ull;
+        continue;
+      }
       read_tile<T, VEC>(t + j * kLen, mx, lane, v[j]);
       if constexpr (FUSED) {
         const int mr = VEC ? 0 : misaligned(static_cast<const T *>(p.res) + row * p.ldres);

@@ -232,6 +232,91 @@ def test_in_place(N, dtype):
     assert all(torch.equal(a, c) for a, c in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("T,N,pad,offset", [(3, 32768, 0, 0), (2, 65536, 8, 0), (3, 65537, 0, 1),
+                                            (9, 70000, 0, 0), (2, 131080, 0, 0)], ids=lambda v: str(v))
+def test_rows_too_long_for_the_chip(T, N, pad, offset, dtype):
+    """Row lengths about the borders of the layouts for long rows, up to those
+    that are read again for each pass."""
+    need_gpu()
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=N, pad=pad, offset=offset)
+    y, s, mean, rstd = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+    assert torch.equal(s, fa.dropout_fwd(x, 0.1, SEED, residual=r))
+    check_fwd(s, w, b, True, y, mean, rstd)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    check_fwd(x, w, b, True, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    check_bwd(dy, x, w, mean, rstd, True, ds, dx, dw, db)
+    dx2, dres, dw2, db2 = fa.dropout_add_layer_norm_bwd(dy, ds, x, w, mean, rstd, 0.1, SEED)
+    assert torch.equal(dres, dx) and torch.equal(dw, dw2) and torch.equal(db, db2)
+    mask = (fa.dropout_fwd(torch.ones_like(dx), 0.1, SEED) != 0).cpu()
+    (full, _, _), (bound, _, _) = R.norm_bwd(*cpu(dy, x, w, mean, rstd), True, ds.cpu())
+    scale = 65536 / (65536 - round(0.1 * 65536))
+    want, b3 = R.drop(full, mask, scale)
+    R.check("dx", dx2, want, torch.where(mask, bound * scale, 0.0) + b3, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 32, 33, 63, 147, 149, 297, 1185, 3553])
+@pytest.mark.parametrize("N", [24, 264, 1024, 8200])
+def test_row_counts_about_the_layouts_borders(T, N):
+    need_gpu()
+    (x, _, dy, ds), w, b = inputs(T, N, torch.bfloat16, seed=T)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    check_fwd(x, w, b, True, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    check_bwd(dy, x, w, mean, rstd, True, ds, dx, dw, db)
+
+
+def test_a_workspace_of_exactly_the_size_asked_for():
+    """The bytes behind it stay as they were, for row counts and lengths of
+    every layout."""
+    need_gpu()
+    for T, N in [(1, 8), (5, 4096), (40, 4096), (500, 4096), (300, 8200), (60, 20000), (40, 40001),
+                 (100, 70000)]:
+        (x, _, dy, _), w, b = inputs(T, N, torch.bfloat16, seed=1)
+        _, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+        n = fa.layer_norm_ws_bytes(T, N)
+        buf = torch.full((n + 4096,), 85, dtype=torch.uint8, device="cuda")
+        got = fa.layer_norm_bwd(dy, x, w, mean, rstd, ws=buf[:n])
+        want = fa.layer_norm_bwd(dy, x, w, mean, rstd)
+        assert torch.all(buf[n:] == 85), (T, N)
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_two_streams_at_once_and_two_graphs_with_a_workspace_each():
+    need_gpu()
+    sets = [inputs(400, 4096, torch.bfloat16, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in sets]
+    want = []
+    for (x, r, dy, ds), w, b in sets:
+        f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+        want.append(f + fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [None, None]
+        for k, ((x, r, dy, ds), w, b) in enumerate(sets):
+            with torch.cuda.stream(streams[k]):
+                f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+                got[k] = f + fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED)
+        torch.cuda.synchronize()
+        for a, c in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, c))
+    graphs, outs = [], []
+    for k, ((x, r, dy, ds), w, b) in enumerate(sets):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[k]):
+            f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+            outs.append(f + fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED))
+        graphs.append(g)
+    for _ in range(5):
+        for k, g in enumerate(graphs):
+            with torch.cuda.stream(streams[k]):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, c in zip(outs, want):
+        assert all(torch.equal(u, v) for u, v in zip(a, c))
+
+
 def test_repeats_bit_for_bit_with_a_dirty_workspace():
     need_gpu()
     T, N = 1000, 4096
