@@ -3,10 +3,11 @@
 // from (key, row, column) where it is needed (rows.cuh) and never stored.
 // The backward pass is the same map of dy under the same key.
 //
-// Bound by memory: two or three accesses of an element against some five
-// integer instructions for its share of the generator.  Each thread has all
-// its loads in flight before it computes, and the grid covers the matrix
-// once.
+// Two or three accesses of an element against some twenty instructions, most
+// of them the generator's: with a residual bound by memory (16384 x 4096 bf16
+// 61.2 us, 6.6 TB/s), without one as much by instructions (8192 x 4096 25.2
+// us, 5.3 TB/s).  Each thread has all its loads in flight before it computes,
+// and the grid covers the matrix once.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,10 +20,11 @@ namespace {
 
 using namespace rows;
 
-#ifndef DROP_U
-#define DROP_U 4
-#endif
 constexpr int kThreads = 256;
+// Rows of a thread where there are enough for every SM: 8192 x 4096 bf16 takes
+// 30.0, 27.9 and 25.2 us with one, two and four.  Few rows are spread over the
+// SMs instead.
+constexpr int kRows = 4;
 
 struct DropoutParams {
   const void *x, *res;
@@ -183,14 +185,14 @@ cudaError_t launch(const DropoutArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.x, a.ldx) && vec_ok(a.y, a.ldy) &&
                    (!a.res || vec_ok(a.res, a.ldres));
   const int64_t per_row = vec ? a.N / 8 : (a.N + kTile - 1) / kTile;
-  const int rows = vec && a.T * per_row > 148 * 8 * kThreads ? DROP_U : 1;
+  const int rows = vec && a.T * per_row > 148 * 8 * kThreads ? kRows : 1;
   const int64_t per_cta = vec ? kThreads : kThreads / 32, units = (a.T + rows - 1) / rows * per_row;
   const int64_t ctas = (units + per_cta - 1) / per_cta;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 4 KB is no GPU's memory
   const DropoutParams p = {a.x, a.res, a.y, a.ldx, a.ldres, a.ldy, a.T, a.N, units,
                            Divisor((uint32_t)per_row),
                            {a.drop.seed, a.drop.step, a.drop.threshold, a.drop.scale}};
-  return launch_pdl(!vec ? dropout_any_kernel<T> : rows == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, DROP_U>,
+  return launch_pdl(!vec ? dropout_any_kernel<T> : rows == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, kRows>,
                     dim3((unsigned)ctas), dim3(kThreads), 0, st, p);
 }
 

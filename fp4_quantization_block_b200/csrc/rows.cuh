@@ -240,9 +240,6 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, int bytes
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest n groups of this thread have arrived.
 __device__ __forceinline__ void cp_async_wait(int n) {
@@ -444,10 +441,8 @@ __device__ __forceinline__ void stage_vec(W *dst, const W *src, int cols, int ro
 // A lane's staged weights of a tile.
 template <typename T, typename W>
 __device__ __forceinline__ void read_vec(const W *tile, int lane, uint64_t (&f)[4]) {
-  if constexpr (sizeof(T) == sizeof(W) || sizeof(W) == 4) {
-    read_tile<W, true>(tile, 0, lane, f);
-  } else {  // 16-bit weights beside binary32 rows are not taken
-  }
+  static_assert(sizeof(W) == 4 || sizeof(T) == sizeof(W), "weights of the rows' type or binary32");
+  read_tile<W, true>(tile, 0, lane, f);
 }
 
 // ------------------------------------------------------------- clusters ---
