@@ -139,13 +139,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   W *const wsm = reinterpret_cast<W *>(smem + (size_t)g.warps * g.teams * g.stages * kStage * sizeof(T));
   const uint32_t q = cid * g.teams + team;
   const int n = g.rows(q);
-  // (backward reads whole rooms: a tile past the row's end is zeros for good)
+  if constexpr (VEC) {  // (tiles past the row's end too: they are read)
 #pragma unroll
-  for (int j = 0; j < CH; ++j)
-    if (left - j * kTile < (VEC ? kTile : 1))
-      for (int s = 0; s < A * g.stages; ++s)
-        clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
-  __syncwarp();
+    for (int j = 0; j < CH; ++j)
+      if (left - j * kTile < kTile)
+        for (int s = 0; s < A * g.stages; ++s)
+          clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
+    __syncwarp();
+  }
   if constexpr (CLUSTER) cluster_arrive();  // all CTAs are there before anything is sent to them
   grid_dependency_wait();
   grid_dependents_launch();
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
       const bool head = !VEC && q == 0 && col == 0 && ahead == n;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        if (!VEC && left - j * kTile <= 0) continue;
+        if (!VEC && left - j * kTile <= 0) break;
         const bool h = head && j == 0;
         fill_tile<T, VEC>(t + j * kLen, fx + j * kTile, left - j * kTile, h, lane);
         fill_tile<T, VEC>(t + (CH + j) * kLen, fdy + j * kTile, left - j * kTile, h, lane);
@@ -233,6 +234,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
         uint64_t dy[4];
+        if (!VEC && left - j * kTile <= 0) {  // past the row's end
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xh[j][i] = gg[j][i] = 0ull;
+          continue;
+        }
         read_tile<T, VEC>(t + j * kLen, mx, lane, xh[j]);
         read_tile<T, VEC>(t + (CH + j) * kLen, md, lane, dy);
 #pragma unroll
@@ -288,9 +294,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
 #pragma unroll
         for (int i = 0; i < 4; ++i) gg[j][i] = f2_fma(xh[j][i], c2, f2_add(gg[j][i], c1));
         if constexpr (DS) {
-          uint64_t r[4];
+          uint64_t r[4] = {};
           const int mr = VEC ? 0 : misaligned(static_cast<const T *>(p.ds) + row * p.ldds);
-          read_tile<T, VEC>(t + (2 * CH + j) * kLen, mr, lane, r);
+          if (VEC || left - j * kTile > 0) read_tile<T, VEC>(t + (2 * CH + j) * kLen, mr, lane, r);
 #pragma unroll
           for (int i = 0; i < 4; ++i) gg[j][i] = f2_fma(gg[j][i], scale, r[i]);
         } else {

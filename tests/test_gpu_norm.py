@@ -207,6 +207,31 @@ def test_extreme_rows(N):
     assert torch.equal(dx[fine], dx2)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("N", [5, 100, 264, 301, 520, 4099, 4104, 8705, 9001])
+def test_rows_of_nan_leave_the_other_rows_alone(N, dtype):
+    """Every fourth row of many is NaN or infinite; the others, which follow
+    them through the same threads and the same memory, come out as if they were
+    not there."""
+    need_gpu()
+    T = 1900
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=N)
+    bad = torch.arange(T, device="cuda") % 4 == 1
+    nan = torch.where(torch.arange(T, device="cuda")[:, None] % 8 == 1, float("nan"), float("inf")).to(dtype)
+    y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    dx, _, _ = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+    f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+    g = fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED)
+    xb, dyb = torch.where(bad[:, None], nan, x), torch.where(bad[:, None], nan, dy)
+    y2, mean2, rstd2 = fa.layer_norm_fwd(xb, w, b, EPS)
+    dx2, _, _ = fa.layer_norm_bwd(dyb, xb, w, mean2, rstd2, dres=ds)
+    f2 = fa.dropout_add_layer_norm_fwd(xb, r, w, b, 0.1, SEED)
+    g2 = fa.dropout_add_layer_norm_bwd(dyb, ds, f2[1], w, f2[2], f2[3], 0.1, SEED)
+    for a, c in ((y, y2), (mean, mean2), (rstd, rstd2), (dx, dx2), (f[0], f2[0]), (f[1], f2[1]),
+                 (g[0], g2[0]), (g[1], g2[1])):
+        assert torch.equal(a[~bad], c[~bad])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("N", [96, 4096, 4099, 17000])
 def test_in_place(N, dtype):
