@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
   float2 *red0 = &red[0][team * g.warps], *red1 = &red[1][team * g.warps];
   const uint32_t q = blockIdx.x * g.teams + team;
   const int n = g.rows(q);
-  if constexpr (VEC) {
+  if constexpr (VEC) {  // (tiles past the row's end too: they are read)
 #pragma unroll
     for (int j = 0; j < CH; ++j)
-      if (left - j * kTile > 0 && left - j * kTile < kTile)
+      if (left - j * kTile < kTile)
         for (int s = 0; s < A * g.stages; ++s)
           clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
     __syncwarp();
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
       const bool head = !VEC && q == 0 && col == 0 && ahead == n;
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
-        if (left - j * kTile <= 0) break;
+        if (!VEC && left - j * kTile <= 0) break;
         fill_tile<T, VEC>(ft + j * kLen, fx + j * kTile, left - j * kTile, head && j == 0, lane);
         if constexpr (FUSED)
           fill_tile<T, VEC>(ft + (CH + j) * kLen, fr + j * kTile, left - j * kTile, head && j == 0, lane);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
     uint64_t v[CH][4], acc = 0ull;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      if (left - j * kTile <= 0) {
+      if (!VEC && left - j * kTile <= 0) {
         v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0ull;
         continue;
       }
@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(fwd_threads(CH, FUSED), 1) norm_fwd_kernel(con
         if (j * kTile + pair_col<T>(lane, 0) >= left) lo = 0ull;
         if (j * kTile + pair_col<T>(lane, 2) >= left) hi = 0ull;
         acc = f2_add(acc, f2_add(lo, hi));
+      } else if ((j + 1) * kTile <= left) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = f2_fma(d[i], d[i], acc);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

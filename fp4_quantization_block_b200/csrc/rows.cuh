@@ -318,6 +318,7 @@ __device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool 
       if (e < left) cp_async16(tile + e, src + e);
     }
   } else {
+    if (left <= 0) return;  // a tile past the row's end
     const int mis = misaligned(src), total = (left < kTile ? left : kTile) * (int)sizeof(T) + mis;
     const char *word0 = reinterpret_cast<const char *>(src) - mis;
 #pragma unroll
@@ -390,6 +391,7 @@ __device__ __forceinline__ void store_tiles(T *stage, T *dst, int left, int lane
       }
     }
   } else {
+    if (left <= 0) return;  // a warp past the row's end
     __syncwarp();  // the stage's last readers
 #pragma unroll
     for (int j = 0; j < CH; ++j) {

@@ -103,7 +103,8 @@ def test_rms_form_and_binary32_weights(T, N, dtype):
 @pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
 @pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1), (5, 3), (2, 2)],
                          ids=lambda v: str(v))
-@pytest.mark.parametrize("N", [40, 771, 4096, 4098, 18433])
+@pytest.mark.parametrize("N", [1, 2, 40, 255, 256, 257, 300, 511, 512, 513, 768, 771, 1279, 1280, 4096, 4098,
+                               4351, 18433])
 def test_leading_dimensions_and_offsets(N, pad, offset, dtype):
     """Strided and offset matrices; what lies between the rows stays as it was."""
     need_gpu()
