@@ -603,6 +603,7 @@ fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_
   a.dw = dweight;
   a.db = dbias;
   a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
+  a.status = static_cast<uint32_t *>(workspace);
   return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
 }
 
@@ -715,6 +716,7 @@ fa4_status fa4_dropout_add_layernorm_bwd(const void *dy, int64_t lddy, const voi
   a.dw = dweight;
   a.db = dbias;
   a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
+  a.status = static_cast<uint32_t *>(workspace);
   return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
 }
 

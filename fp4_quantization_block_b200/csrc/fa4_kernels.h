@@ -127,6 +127,7 @@ struct NormBwdArgs {
   int64_t lddx, lddres;
   float *dw, *db;
   float *partials;  // norm_partials_count(T, N) * 2 * N
+  uint32_t *status;  // bounded-wait status word
   DropArgs drop;
 };
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t st);

@@ -16,6 +16,7 @@ struct BwdParams {
   int64_t lddx, lddres;
   float *partials;  // [cluster][2][N]
   float *dw, *db;   // where there is one cluster only
+  uint32_t *status;  // set when a wait within a cluster gives up
   int one;
   Drop drop;
   int64_t step_x, step_dy, step_ds, step_dx, step_dres;  // elements between a team's rows
@@ -112,7 +113,11 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(const BwdParams p) {
 // of the whole row between them; xh and g stay in registers.  CLUSTER: rows
 // too wide for a CTA are shared by a cluster of CTAs, each with some of the
 // columns (and fewer partial sums to write): every warp sends its part of the
-// two sums to all of them.
+// two sums to all of them, and each team waits at a barrier of its own for the
+// parts of its row, not for another team or for a fence over its stores.  Two
+// barriers and two buffers take turns: a part of the row after the next one is
+// sent only when all parts of the next one have come, and a warp sends its own
+// only after it has read this row's.
 //
 // 8192 x 4096 bf16 with ds takes 47.8 us (5.6 TB/s; 65536 rows 6.9 TB/s):
 // nearly 10 us are a launch's own, the first row's latency, the last row's,
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kParts = CLUSTER ? 8 * kBwdWarps : kBwdWarps;
   __shared__ float2 red[2][kParts];  // [row buffer][team][CTA][warp]
+  __shared__ uint64_t arrived[2][CLUSTER ? kBwdWarps : 1];  // [row buffer][team]
   constexpr int A = DS ? 3 : 2, kLen = kTileLen<T, VEC>, kStage = A * CH * kLen;
   const int lane = threadIdx.x & 31, cta_warp = threadIdx.x >> 5;
   const int team = cta_warp / g.warps, warp = cta_warp - team * g.warps;
@@ -147,7 +153,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
           clear_tail(ring + (s * CH + j) * kLen, left - j * kTile, kLen, lane);
     __syncwarp();
   }
-  if constexpr (CLUSTER) cluster_arrive();  // all CTAs are there before anything is sent to them
+  if constexpr (CLUSTER) {  // all CTAs and their barriers are there before anything is sent to them
+    if (threadIdx.x < 2 * kBwdWarps) barrier_init(&arrived[0][0] + threadIdx.x);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    cluster_sync();
+  }
   grid_dependency_wait();
   grid_dependents_launch();
   const int cols = (int)p.N - rank * room;
@@ -197,7 +208,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   const float inv_n = 1.0f / (float)p.N;
   T *dx = static_cast<T *>(p.dx) + q * p.lddx + col;
   T *dres = FUSED ? static_cast<T *>(p.dres) + q * p.lddres + col : nullptr;
-  if constexpr (CLUSTER) cluster_wait();
 
   const int parts = CLUSTER ? g.cluster * g.warps : g.warps;  // of a row's sums
   cp_async_wait(g.stages > 1 ? g.stages - 2 : 0);             // the oldest group holds the weight
@@ -208,9 +218,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   const bool upper = lane >= 16;  // the lanes that add up the second sum
   int ts = 0;
   uint32_t row = q;
-  // the CTAs of a cluster, and its teams, go through the same number of rows
-  const int rounds = CLUSTER ? g.rows(cid * g.teams) : n;
-  for (int k = 0; k < rounds; ++k) {
+  for (int k = 0; k < n; ++k) {
     __syncwarp();  // the stage filled next was read by the whole warp
     fill();
     const float rstd = rstd_next, mean = mean_next;
@@ -227,7 +235,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
     T *const t = ring + ts;
     const uint64_t scale = f2_set(rstd);
     uint64_t xh[CH][4], gg[CH][4], s1 = 0ull, s2 = 0ull;
-    if (!CLUSTER || k < n) {
+    {
       const uint64_t shift = f2_set(-mean);
       const int mx = VEC ? 0 : misaligned(static_cast<const T *>(p.x) + row * p.ldx);
       const int md = VEC ? 0 : misaligned(static_cast<const T *>(p.dy) + row * p.lddy);
@@ -264,10 +272,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
     if (parts > 1) {
       const int l = lane & 15;
       if constexpr (CLUSTER) {
+        uint64_t *const barrier = &arrived[k & 1][team];
         const float2 both = make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
-        if (lane < g.cluster) cluster_store(&red0[rank * g.warps + warp], lane, both);
-        cluster_arrive();
-        cluster_wait();
+        if (warp == 0 && lane == 0) barrier_expect(barrier, 8 * parts);
+        if (lane < g.cluster) cluster_send(&red0[rank * g.warps + warp], barrier, lane, both);
+        // (a wait ends by itself; what a lane saw decides for the warp)
+        if (!__all_sync(0xFFFFFFFFu, barrier_wait(barrier, (k >> 1) & 1))) {
+          if (lane == 0) *p.status = 7u;
+          break;
+        }
         v = 0.0f;
         for (int i = l; i < parts; i += 16) v += upper ? red0[i].y : red0[i].x;
 #pragma unroll
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
     }
     v *= -inv_n;
     const float m1 = __shfl_sync(0xFFFFFFFFu, v, 0), m2 = __shfl_sync(0xFFFFFFFFu, v, 16);
-    if (!CLUSTER || k < n) {
+    {
       const uint64_t c1 = f2_set(p.center ? m1 : 0.0f), c2 = f2_set(m2);
 #pragma unroll
       for (int j = 0; j < CH; ++j) {
@@ -318,6 +331,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
     ts = ts + kStage == ring_len ? 0 : ts + kStage;
   }
 
+  if constexpr (CLUSTER) {  // nobody leaves while something may still be sent to them
+    __syncwarp();
+    cluster_sync();
+  }
   // the teams' sums, through the ring's memory, in the teams' order
   float *const out_w = p.one ? p.dw : p.partials + (int64_t)cid * 2 * p.N;
   float *const out_b = p.one ? p.db : out_w + p.N;
@@ -424,6 +441,7 @@ cudaError_t backward_w(const NormBwdArgs &a, int *n, cudaStream_t st) {
   p.lddres = a.lddres;
   p.partials = a.partials;
   p.dw = a.dw;
+  p.status = a.status;
   p.db = a.db;
   p.drop = make_drop(a.drop);
   auto go = [&](auto v, auto f) {

@@ -448,19 +448,53 @@ __device__ __forceinline__ void read_vec(const W *tile, int lane, uint64_t (&f)[
 }
 
 // ------------------------------------------------------------- clusters ---
-// Writes v to the same place of the shared memory of the cluster's CTA `rank`.
-__device__ __forceinline__ void cluster_store(float2 *place, int rank, float2 v) {
+// The CTAs of a cluster exchange small sums by asynchronous stores that count
+// their bytes at a barrier beside the place they go to: the receivers wait for
+// exactly these, and no fence waits for the senders' stores to memory.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
   uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(place)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
 }
-// The two halves of a barrier of all threads of a cluster (of the CTA where
-// there is none): what was written before the arrival is seen after the wait.
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+// Sends v to the same place of the CTA `rank`, eight bytes at its barrier.
+__device__ __forceinline__ void cluster_send(float2 *place, uint64_t *barrier, int rank, float2 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+                   cluster_addr(smem_addr(place), rank)),
+               "f"(v.x), "f"(v.y), "r"(cluster_addr(smem_addr(barrier), rank))
+               : "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void barrier_init(uint64_t *barrier) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(barrier)) : "memory");
+}
+// The one arrival of a phase, and the bytes that the phase waits for.
+__device__ __forceinline__ void barrier_expect(uint64_t *barrier, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(barrier)), "r"(bytes)
+               : "memory");
+}
+// Waits for a phase; false if it did not complete within some seconds.
+__device__ __forceinline__ bool barrier_wait(uint64_t *barrier, uint32_t parity) {
+  const uint32_t addr = smem_addr(barrier);
+  uint64_t begin = 0, now;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 255u) == 255u) {
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (begin == 0) begin = now;
+      if (now - begin > 2000000000ull) return false;
+    }
+  }
+}
+// A barrier of all threads of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace rows

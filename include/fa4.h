@@ -372,7 +372,10 @@ FA4_API fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int6
  * [N]; dbias may be NULL).  The sums over the rows are taken in a fixed order:
  * a call repeats bit for bit.  dx may be dy, x or dres itself (same leading
  * dimension).  Workspace: fa4_layernorm_ws_bytes (nothing in it has to be
- * zero); calls that may run at the same time need one each.
+ * zero); calls that may run at the same time need one each.  A bounded wait
+ * that gives up (rows shared by a cluster) sets the header's status word and
+ * leaves the outputs incomplete: zero the header first to read it with
+ * fa4_check_device_status.
  * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (w_dtype), WORKSPACE, CUDA. */
 FA4_API fa4_status fa4_layernorm_ws_bytes(int64_t T, int64_t N, size_t *workspace_bytes);
 FA4_API fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
