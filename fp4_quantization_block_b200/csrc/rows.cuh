@@ -319,8 +319,15 @@ __device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool 
     }
   } else {
     if (left <= 0) return;  // a tile past the row's end
-    const int mis = misaligned(src), total = (left < kTile ? left : kTile) * (int)sizeof(T) + mis;
+    const int mis = misaligned(src);
     const char *word0 = reinterpret_cast<const char *>(src) - mis;
+    if (left >= kTile + kPer16 && !(head && mis)) {  // every word whole, and the one after them
+#pragma unroll
+      for (int i = 0; i < kWords; i += 32) cp_async16(tile + (i + lane) * kPer16, word0 + 16 * (i + lane));
+      if (lane == 0) cp_async16(tile + kTile, word0 + 16 * kWords);
+      return;
+    }
+    const int total = (left < kTile ? left : kTile) * (int)sizeof(T) + mis;
 #pragma unroll
     for (int i = 0; i < kWords + 1; i += 32) {
       const int w = i + lane;
@@ -330,8 +337,7 @@ __device__ __forceinline__ void fill_tile(T *tile, const T *src, int left, bool 
         const int off = mis / (int)sizeof(T);
         for (int e = 0; e < kPer16 - off; ++e) tile[off + e] = e < left ? src[e] : from_float<T>(0.0f);
       } else {
-        cp_async16(tile + w * kPer16, bytes > 0 ? word0 + 16 * w : reinterpret_cast<const char *>(src),
-                   bytes < 0 ? 0 : bytes > 16 ? 16 : bytes);
+        cp_async16(tile + w * kPer16, bytes > 0 ? word0 + 16 * w : word0, bytes < 0 ? 0 : bytes > 16 ? 16 : bytes);
       }
     }
   }
