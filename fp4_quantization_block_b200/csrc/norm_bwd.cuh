@@ -119,15 +119,16 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(const BwdParams p) {
 // sent only when all parts of the next one have come, and a warp sends its own
 // only after it has read this row's.
 //
-// 8192 x 4096 bf16 with ds takes 47.8 us (5.6 TB/s; 65536 rows 6.9 TB/s):
+// 8192 x 4096 bf16 with ds takes 47.8 us (5.6 TB/s; 65536 rows 7.0 TB/s):
 // nearly 10 us are a launch's own, the first row's latency, the last row's,
-// the sums at the end and the second launch.  Fused with dropout 68.6 us:
+// the sums at the end and the second launch.  Fused with dropout 68.5 us:
 // half of all issue slots are used, by 16 warps of 128 registers (the sums of
-// dw and db are 32 of them).  Wide rows wait for the cluster's exchange: 1000
-// x 14336 fp16 36.6 us, 2.35 TB/s.  Tried and slower: a cluster for all rows
-// (65 us at 4096 x 8192 against 46), the second pass computing xh and g again
-// beside a barrier split in two (67 us), four chunks a thread (53 us at 4096 x
-// 8192), the dropout's bits before the data (74 -> 85 us).
+// dw and db are 32 of them).  Wide rows: 1000 x 14336 fp16 35.0 us, 2.5 TB/s;
+// 2000 x 24576 bf16 91 us (115 with a barrier of the whole cluster at each
+// row, which also waits for the stores of dx).  Tried and slower: clusters of
+// two for rows that fit a CTA (50 us at 4096 x 8192 against 45), the second
+// pass computing xh and g again (67 us at 8192 x 4096), four chunks a thread
+// (53 us at 4096 x 8192), the dropout's bits before the data (fused 85 us).
 template <typename T, typename W, int CH, bool VEC, bool FUSED, bool DS, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdParams p, const Layout g) {
   extern __shared__ __align__(16) unsigned char smem[];

@@ -370,6 +370,77 @@ def test_many_rows_and_offsets_past_32_bits():
     R.check("dx", dx[rows], dxe, bx, dx.dtype)
 
 
+@pytest.mark.parametrize("dtype,wtype", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                         (torch.float16, torch.float16), (torch.float32, torch.float32)],
+                         ids=["bf16", "bf16-w32", "fp16", "fp32"])
+@pytest.mark.parametrize("N", [7, 512, 1032, 4096, 4099, 9000, 70000])
+def test_weights_off_16_byte_boundaries_and_gradients_in_the_callers_tensors(N, dtype, wtype):
+    need_gpu()
+    T = 40
+    (x, r, dy, ds), w, b = inputs(T, N, dtype, seed=N, wtype=wtype)
+    wide = torch.zeros(2 * N + 16, dtype=wtype, device="cuda")
+    w1, b1 = wide[1:N + 1], wide[N + 4:2 * N + 4]
+    w1.copy_(w)
+    b1.copy_(b)
+    y, mean, rstd = fa.layer_norm_fwd(x, w1, b1, EPS)
+    check_fwd(x, w, b, True, y, mean, rstd)
+    grads = torch.full((2 * N + 9,), 7.0, device="cuda")
+    dw, db = grads[1:N + 1], grads[N + 5:2 * N + 5]
+    dx, gw, gb = fa.layer_norm_bwd(dy, x, w1, mean, rstd, dres=ds, dweight=dw, dbias=db)
+    assert gw is dw and gb is db
+    check_bwd(dy, x, w, mean, rstd, True, ds, dx, dw, db)
+    assert grads[0] == 7.0 and torch.all(grads[N + 1:N + 5] == 7.0) and torch.all(grads[2 * N + 5:] == 7.0)
+    assert torch.equal(wide[N + 1:N + 4], torch.zeros_like(wide[N + 1:N + 4]))
+
+
+def test_single_rows_and_columns_of_any_stride():
+    """One row's stride means nothing, one column's either."""
+    need_gpu()
+    big = torch.randn(64, 4096, device="cuda")
+    w, b = torch.rand(64, device="cuda") + 0.5, torch.rand(64, device="cuda")
+    row = big.t()[5:6, :]  # strides (1, 4096): no unit column stride
+    with pytest.raises(ValueError):
+        fa.layer_norm_fwd(row, w, b)
+    one = torch.as_strided(big, (1, 64), (3, 1), 7)
+    y, mean, rstd = fa.layer_norm_fwd(one, w, b)
+    check_fwd(one, w, b, True, y, mean, rstd)
+    col = big[:, 9:10]
+    y, mean, rstd = fa.layer_norm_fwd(col, w[:1], b[:1], center=False)
+    check_fwd(col, w[:1], b[:1], False, y, mean, rstd)
+    dx, dw, db = fa.layer_norm_bwd(col, col, w[:1], None, rstd, center=False)
+    check_bwd(col, col, w[:1], None, rstd, False, None, dx, dw, db)
+    thin = big[0:1, :].t()  # [4096, 1], strides (1, 4096)
+    assert torch.equal(fa.dropout_fwd(thin, 0.5, 3), fa.dropout_fwd(thin.contiguous(), 0.5, 3))
+
+
+def test_wide_rows_captured_and_replayed():
+    """Rows shared by clusters, and few rows in one cluster, in a graph."""
+    need_gpu()
+    for T, N in ((50, 12296), (6, 4096), (70, 20001)):
+        (x, r, dy, ds), w, b = inputs(T, N, torch.bfloat16, seed=T)
+        f = fa.dropout_add_layer_norm_fwd(x, r, w, b, 0.1, SEED)
+        want = fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = fa.dropout_add_layer_norm_bwd(dy, ds, f[1], w, f[2], f[3], 0.1, SEED)
+        for _ in range(3):
+            for t in got:
+                t.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_device_status_of_a_zeroed_workspace_is_clean():
+    need_gpu()
+    (x, _, dy, ds), w, b = inputs(100, 20000, torch.bfloat16, seed=4)
+    _, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    ws = fa.workspace(fa.layer_norm_ws_bytes(100, 20000))
+    fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds, ws=ws)
+    assert fa.check_device_status(ws) == 0
+
+
 def test_another_stream():
     need_gpu()
     (x, r, dy, ds), w, b = inputs(500, 4096, torch.bfloat16, seed=2)
