@@ -593,17 +593,15 @@ def gemm_mxout(A: QTensor, B: QTensor, alpha: float = 1.0, store_d: bool = True,
 DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
-def _on_first_device(fn):
-    """_on_tensor_device for the calls whose first argument is a matrix: small
-    calls of theirs cost what their checks cost."""
-    @functools.wraps(fn)
-    def wrapped(*args, **kwargs):
-        x = args[0] if args else next(iter(kwargs.values()), None)
-        if isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(x.device):
-                return fn(*args, **kwargs)
-        return fn(*args, **kwargs)
-    return wrapped
+def _elsewhere(x: torch.Tensor) -> bool:
+    """Whether the CUDA tensor x is on another device than the current one.
+    These calls ask it themselves instead of through _on_tensor_device: small
+    ones cost what their checks cost."""
+    return x.get_device() != torch.cuda.current_device()
+
+
+def _stream_of(x: torch.Tensor):
+    return _stream(x.device) if _raw_stream is None else _raw_stream(x.get_device())
 
 
 def _rows(x: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
@@ -705,7 +703,6 @@ def _norm_ws(ws, x):
     return ws
 
 
-@_on_first_device
 def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
                    eps: float = 1e-5, center: bool = True, out: torch.Tensor | None = None
                    ) -> tuple[torch.Tensor, torch.Tensor | None, torch.Tensor]:
@@ -714,17 +711,19 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     RMS form: no mean (None).  weight and bias are of x's type or float32.
     out may be x."""
     ldx = _rows(x, "x")
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return layer_norm_fwd(x, weight, bias, eps, center, out)
     wd = _weights(weight, bias, x)
     y, ldy = _out_rows(out, "out", x)
     T, N = x.shape
     mean, rstd = _new_stats(x, center)
     _check(lib().fa4_layernorm_fwd(_ptr(x), ldx, T, N, DTYPE[x.dtype], _ptr(weight), _ptr(bias), wd,
                                    eps, 1 if center else 0, _ptr(y), ldy, _ptr(mean), _ptr(rstd),
-                                   _stream(x.device)), "fa4_layernorm_fwd")
+                                   _stream_of(x)), "fa4_layernorm_fwd")
     return y, mean, rstd
 
 
-@_on_first_device
 def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                    mean: torch.Tensor | None, rstd: torch.Tensor, center: bool = True,
                    bias_grad: bool = True, dres: torch.Tensor | None = None,
@@ -736,6 +735,10 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     float32 sums over the rows in a fixed order (dbias None without
     bias_grad)."""
     ldx, lddy = _rows(x, "x"), _rows(dy, "dy", x)
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return layer_norm_bwd(dy, x, weight, mean, rstd, center, bias_grad, dres, dx, dweight,
+                                  dbias, ws)
     wd = _weights(weight, None, x)
     _stats(mean, rstd, center, x)
     ldr = 0 if dres is None else _rows(dres, "dres", x)
@@ -747,11 +750,10 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                                    DTYPE[x.dtype], _ptr(weight), wd, 1 if center else 0,
                                    _ptr(mean) if center else None, _ptr(rstd), _ptr(dx), lddx,
                                    _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel(),
-                                   _stream(x.device)), "fa4_layernorm_bwd")
+                                   _stream_of(x)), "fa4_layernorm_bwd")
     return dx, dweight, dbias
 
 
-@_on_first_device
 def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None
                 ) -> torch.Tensor:
@@ -761,28 +763,32 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None 
     for graphs that draw a new mask at each replay.  out may be x or
     residual."""
     ldx = _rows(x, "x")
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return dropout_fwd(x, p, seed, step, residual, out)
     ldr = 0 if residual is None else _rows(residual, "residual", x)
     y, ldy = _out_rows(out, "out", x)
     _check(lib().fa4_dropout_fwd(_ptr(x), ldx, _ptr(residual), ldr, x.shape[0], x.shape[1],
                                  DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF, _step(step, x),
-                                 _ptr(y), ldy, _stream(x.device)), "fa4_dropout_fwd")
+                                 _ptr(y), ldy, _stream_of(x)), "fa4_dropout_fwd")
     return y
 
 
-@_on_first_device
 def dropout_bwd(dy: torch.Tensor, p: float, seed: int, step: torch.Tensor | None = None,
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """dx of dropout_fwd under the same p, seed and step (the residual's
     gradient is dy itself).  out may be dy."""
     lddy = _rows(dy, "dy")
+    if _elsewhere(dy):
+        with torch.cuda.device(dy.device):
+            return dropout_bwd(dy, p, seed, step, out)
     dx, lddx = _out_rows(out, "out", dy)
     _check(lib().fa4_dropout_bwd(_ptr(dy), lddy, dy.shape[0], dy.shape[1], DTYPE[dy.dtype], p,
                                  seed & 0xFFFFFFFFFFFFFFFF, _step(step, dy), _ptr(dx), lddx,
-                                 _stream(dy.device)), "fa4_dropout_bwd")
+                                 _stream_of(dy)), "fa4_dropout_bwd")
     return dx
 
 
-@_on_first_device
 def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
                                bias: torch.Tensor | None, p: float, seed: int,
                                step: torch.Tensor | None = None, eps: float = 1e-5,
@@ -793,6 +799,10 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
     as dropout_fwd gives it, y = the layer norm of the stored s.  s may be
     residual and out may be x."""
     ldx, ldr = _rows(x, "x"), _rows(residual, "residual", x)
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return dropout_add_layer_norm_fwd(x, residual, weight, bias, p, seed, step, eps, center,
+                                              out, s)
     wd = _weights(weight, bias, x)
     (y, ldy), (s, lds) = _out_rows(out, "out", x), _out_rows(s, "s", x)
     T, N = x.shape
@@ -800,11 +810,10 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
     _check(lib().fa4_dropout_add_layernorm_fwd(
         _ptr(x), ldx, _ptr(residual), ldr, T, N, DTYPE[x.dtype], p, seed & 0xFFFFFFFFFFFFFFFF,
         _step(step, x), _ptr(weight), _ptr(bias), wd, eps, 1 if center else 0, _ptr(s), lds, _ptr(y),
-        ldy, _ptr(mean), _ptr(rstd), _stream(x.device)), "fa4_dropout_add_layernorm_fwd")
+        ldy, _ptr(mean), _ptr(rstd), _stream_of(x)), "fa4_dropout_add_layernorm_fwd")
     return y, s, mean, rstd
 
 
-@_on_first_device
 def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: torch.Tensor,
                                weight: torch.Tensor, mean: torch.Tensor | None, rstd: torch.Tensor,
                                p: float, seed: int, step: torch.Tensor | None = None,
@@ -818,6 +827,10 @@ def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: tor
     that reaches s by another way, or None); dx = dropout of that sum under
     the same p, seed and step."""
     lds, lddy = _rows(s, "s"), _rows(dy, "dy", s)
+    if _elsewhere(s):
+        with torch.cuda.device(s.device):
+            return dropout_add_layer_norm_bwd(dy, ds, s, weight, mean, rstd, p, seed, step, center,
+                                              bias_grad, dx, dres, dweight, dbias, ws)
     ldds = 0 if ds is None else _rows(ds, "ds", s)
     wd = _weights(weight, None, s)
     _stats(mean, rstd, center, s)
@@ -829,16 +842,18 @@ def dropout_add_layer_norm_bwd(dy: torch.Tensor, ds: torch.Tensor | None, s: tor
         _ptr(dy), lddy, _ptr(ds), ldds, _ptr(s), lds, T, N, DTYPE[s.dtype], p,
         seed & 0xFFFFFFFFFFFFFFFF, _step(step, s), _ptr(weight), wd, 1 if center else 0,
         _ptr(mean) if center else None, _ptr(rstd), _ptr(dx), lddx, _ptr(dres), lddr, _ptr(dweight),
-        _ptr(dbias), _ptr(ws), ws.numel(), _stream(s.device)), "fa4_dropout_add_layernorm_bwd")
+        _ptr(dbias), _ptr(ws), ws.numel(), _stream_of(s)), "fa4_dropout_add_layernorm_bwd")
     return dx, dres, dweight, dbias
 
 
-@_on_first_device
 def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """dz[T, 2F] of the SwiGLU producer (swiglu_quantize) from the gradient
     dh[T, F] of h: the dY that linear_bwd of the gate+up linear takes.  out
     may be z."""
     ldz, lddh = _as_bf16_2d(z, "z"), _as_bf16_2d(dh, "dh")
+    if _elsewhere(z):
+        with torch.cuda.device(z.device):
+            return swiglu_bwd(z, dh, out)
     T, F2 = z.shape
     if F2 % 2 or dh.shape != (T, F2 // 2) or dh.device != z.device:
         raise ValueError(f"z must hold gate and up halves and dh must be [{T}, {F2 // 2}] on {z.device}")
@@ -847,5 +862,5 @@ def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = Non
     else:
         _check_out(out, (T, F2), (torch.bfloat16,), z.device, "out", row_stride=True)
     _check(lib().fa4_swiglu_bwd(_ptr(z), ldz, _ptr(dh), lddh, T, F2 // 2, _ptr(out), out.stride(0),
-                                _stream(z.device)), "fa4_swiglu_bwd")
+                                _stream_of(z)), "fa4_swiglu_bwd")
     return out
