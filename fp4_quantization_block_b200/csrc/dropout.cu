@@ -25,6 +25,10 @@ constexpr int kThreads = 256;
 // 30.0, 27.9 and 25.2 us with one, two and four.  Few rows are spread over the
 // SMs instead.
 constexpr int kRows = 4;
+// Tiles of a warp of 16-bit rows off 16-byte boundaries: four rows, or two and
+// their residuals (8192 x 4099 bf16 41.4 us, with one row 46.5, element by
+// element 46.5; with residual 53.3).
+constexpr int kTiles = 4;
 
 struct DropoutParams {
   const void *x, *res;
@@ -127,12 +131,70 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutParams p
   }
 }
 
-// Any rows: a warp takes 256 columns of a row, element by element in column
-// order (lane l the columns l, 32 + l, ...), so that its accesses are
+// 16-bit rows off 16-byte boundaries: a warp takes 256 columns of ROWS
+// consecutive rows, by the aligned words that they lie in (rows.cuh), so that a
+// lane has a whole block of the generator.  The words of all rows are on their
+// way together; each row's bits are computed before its words are waited for.
+template <typename T, int ROWS, bool RES>
+__global__ void __launch_bounds__(kThreads) dropout_shifted_kernel(const DropoutParams p) {
+  static_assert(sizeof(T) == 2, "");
+  __shared__ __align__(16) T tiles[kThreads / 32][ROWS][RES ? 2 : 1][kTileLen<T, false>];
+  const int lane = threadIdx.x & 31;
+  const uint32_t warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / 32);
+  const int64_t group0 = p.units < (int64_t(1) << 31) ? p.per_row.quotient((uint32_t)first) : first / p.per_row.d;
+  if (first + warp >= p.units) return;
+  int64_t row;
+  uint32_t unit;
+  place(p, group0, (uint32_t)(first - group0 * p.per_row.d), warp, row, unit);
+  row *= ROWS;
+  const int64_t col = (int64_t)unit * kTile;
+  const int left = (int)(p.N - col), rows = p.T - row < ROWS ? (int)(p.T - row) : ROWS;
+  const T *x = static_cast<const T *>(p.x) + row * p.ldx + col;
+  const T *res = static_cast<const T *>(p.res) + (RES ? row * p.ldres + col : 0);
+  T *y = static_cast<T *>(p.y) + row * p.ldy + col;
+  const bool head = row == 0 && col == 0;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    if (k < rows) {
+      fill_tile<T, false>(tiles[warp][k][0], x + k * p.ldx, left, head && k == 0, lane);
+      if constexpr (RES) fill_tile<T, false>(tiles[warp][k][RES], res + k * p.ldres, left, head && k == 0, lane);
+    }
+    cp_async_commit();
+  }
+  const uint64_t key = p.drop.key();
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k)
+    if (k < rows) {
+      uint32_t w[4];
+      if (p.drop.threshold) {
+        const u32x4 b = philox(unit * (kTile / 8) + lane, (uint32_t)row + k, 0u, kDropTag, (uint32_t)key,
+                               (uint32_t)(key >> 32));
+        w[0] = b.x, w[1] = b.y, w[2] = b.z, w[3] = b.w;
+      }
+      cp_async_wait(ROWS - 1 - k);
+      __syncwarp();
+      uint64_t f[1][4];
+      read_tile<T, false>(tiles[warp][k][0], misaligned(x + k * p.ldx), lane, f[0]);
+      if (p.drop.threshold) drop_pairs(p.drop, w, f[0]);
+      if constexpr (RES) {
+        uint64_t g[4];
+        read_tile<T, false>(tiles[warp][k][RES], misaligned(res + k * p.ldres), lane, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[0][i] = f2_add(f[0][i], g[i]);
+      }
+      store_tiles<T, 1, false>(tiles[warp][k][0], y + k * p.ldy, left, lane, f);
+    }
+}
+
+// Other binary32 rows: a warp takes 256 columns of a row, element by element in
+// column order (lane l the columns l, 32 + l, ...), so that its accesses are
 // consecutive; lane l computes the bits of block l of the tile, and each
 // element takes its bit from the lane that has it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_any_kernel(const DropoutParams p) {
+__global__ void __launch_bounds__(kThreads) dropout_elements_kernel(const DropoutParams p) {
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_dependents_launch();
@@ -185,15 +247,25 @@ cudaError_t launch(const DropoutArgs &a, cudaStream_t st) {
   const bool vec = a.N % 8 == 0 && vec_ok(a.x, a.ldx) && vec_ok(a.y, a.ldy) &&
                    (!a.res || vec_ok(a.res, a.ldres));
   const int64_t per_row = vec ? a.N / 8 : (a.N + kTile - 1) / kTile;
-  const int rows = vec && a.T * per_row > 148 * 8 * kThreads ? kRows : 1;
-  const int64_t per_cta = vec ? kThreads : kThreads / 32, units = (a.T + rows - 1) / rows * per_row;
+  const int64_t per_cta = vec ? kThreads : kThreads / 32;
+  const bool many = a.T * per_row > 148 * 8 * per_cta;
+  // rows of a thread
+  const int rows = !many || (!vec && sizeof(T) == 4) ? 1 : vec ? kRows : a.res ? kTiles / 2 : kTiles;
+  const int64_t units = (a.T + rows - 1) / rows * per_row;
   const int64_t ctas = (units + per_cta - 1) / per_cta;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // 2^31 x 4 KB is no GPU's memory
   const DropoutParams p = {a.x, a.res, a.y, a.ldx, a.ldres, a.ldy, a.T, a.N, units,
                            Divisor((uint32_t)per_row),
                            {a.drop.seed, a.drop.step, a.drop.threshold, a.drop.scale}};
-  return launch_pdl(!vec ? dropout_any_kernel<T> : rows == 1 ? dropout_kernel<T, 1> : dropout_kernel<T, kRows>,
-                    dim3((unsigned)ctas), dim3(kThreads), 0, st, p);
+  void (*kern)(DropoutParams) = many ? dropout_kernel<T, kRows> : dropout_kernel<T, 1>;
+  if (!vec) {
+    if constexpr (sizeof(T) == 2)
+      kern = a.res ? (many ? dropout_shifted_kernel<T, kTiles / 2, true> : dropout_shifted_kernel<T, 1, true>)
+                   : (many ? dropout_shifted_kernel<T, kTiles, false> : dropout_shifted_kernel<T, 1, false>);
+    else
+      kern = dropout_elements_kernel<T>;
+  }
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace

@@ -89,6 +89,31 @@ def test_dropped_infinities_and_nan_leave_no_trace():
     assert torch.equal(fa.dropout_fwd(bad, 0.5, 9), clean)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("T,N,pad,offset", [(1501, 4099, 0, 0), (1502, 4096, 3, 1), (40003, 257, 0, 0),
+                                            (1500, 4090, 2, 2), (4001, 1000, 0, 3)], ids=lambda v: str(v))
+def test_many_unaligned_rows_are_those_of_an_aligned_matrix(T, N, pad, offset, dtype):
+    """The mask depends on the row and the column alone: the first N columns of
+    a wider, aligned matrix come out the same bits, alone, with a residual and
+    in place, and nothing around the rows changes."""
+    need_gpu()
+    M = -(-N // 8) * 8 + 8
+    g = torch.Generator(device="cuda").manual_seed(N)
+    wide = [torch.randn(T, M, generator=g, device="cuda").to(dtype) for _ in range(2)]
+    x, r = (held(m[:, :N], dtype, pad, offset) for m in wide)
+    out = held(torch.zeros(1, 1).expand(T, N), dtype, pad, offset, fill=7.0)
+    want = fa.dropout_fwd(wide[0], 0.1, SEED)[:, :N]
+    assert torch.equal(fa.dropout_fwd(x, 0.1, SEED, out=out), want)
+    want = fa.dropout_fwd(wide[0], 0.1, SEED, residual=wide[1])[:, :N]
+    assert torch.equal(fa.dropout_fwd(x, 0.1, SEED, residual=r, out=out), want)
+    whole = torch.as_strided(out, (T, N + pad), (N + pad, 1), out.storage_offset())
+    assert torch.all(whole[:, N:] == 7.0)
+    assert torch.all(torch.as_strided(out, (64,), (1,), out.storage_offset() + T * (N + pad)) == 7.0)
+    a, c = x.clone(), r.clone()
+    assert torch.equal(fa.dropout_fwd(x, 0.1, SEED, residual=c, out=c), want)
+    assert torch.equal(fa.dropout_fwd(a, 0.1, SEED, residual=r, out=a), want)
+
+
 @pytest.mark.parametrize("N", [64, 1001])
 def test_dropout_in_place(N):
     need_gpu()
