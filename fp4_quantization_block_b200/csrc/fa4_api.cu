@@ -241,6 +241,10 @@ fa4_status make_drop(double p, uint64_t seed, const uint64_t *step, fa4::DropArg
   d->scale = (float)(65536.0 / (65536.0 - d->threshold));
   return FA4_OK;
 }
+// An output in place of an input takes the input's rows, no others.
+inline bool other_rows(const void *out, int64_t ldo, const void *in, int64_t ldi, int64_t T) {
+  return out == in && ldo != ldi && T > 1;
+}
 size_t norm_ws(int64_t T, int64_t N) {
   return kHdr + align256(sizeof(float) * 2 * (size_t)N * (size_t)fa4::norm_partials_count(T, N));
 }
@@ -541,6 +545,7 @@ fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int64_t N, f
       (s = check_weights(weight, bias, w_dtype, dtype)) != FA4_OK ||
       (s = check_stats(mean, rstd, center)) != FA4_OK)
     return s;
+  if (other_rows(y, ldy, x, ldx, T)) return FA4_ERR_INVALID_ARG;
   fa4::NormFwdArgs a = {};
   a.fused = false;
   a.dtype = dtype;
@@ -582,6 +587,9 @@ fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_
       (s = check_stats(mean, rstd, center)) != FA4_OK ||
       (s = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
     return s;
+  if (other_rows(dx, lddx, dy, lddy, T) || other_rows(dx, lddx, x, ldx, T) ||
+      other_rows(dx, lddx, dres, lddres, T))
+    return FA4_ERR_INVALID_ARG;
   fa4::NormBwdArgs a = {};
   a.fused = false;
   a.dtype = dtype;
@@ -618,6 +626,7 @@ fa4_status fa4_dropout_fwd(const void *x, int64_t ldx, const void *residual, int
       (s = check_rows(y, ldy, N, dtype)) != FA4_OK ||
       (s = make_drop(p, seed, step, &a.drop)) != FA4_OK)
     return s;
+  if (other_rows(y, ldy, x, ldx, T) || other_rows(y, ldy, residual, ldres, T)) return FA4_ERR_INVALID_ARG;
   a.dtype = dtype;
   a.T = T;
   a.N = N;
@@ -652,6 +661,9 @@ fa4_status fa4_dropout_add_layernorm_fwd(const void *x, int64_t ldx, const void 
       (e = check_stats(mean, rstd, center)) != FA4_OK ||
       (e = make_drop(p, seed, step, &a.drop)) != FA4_OK)
     return e;
+  if (y == s || other_rows(y, ldy, x, ldx, T) || other_rows(y, ldy, residual, ldres, T) ||
+      other_rows(s, lds, x, ldx, T) || other_rows(s, lds, residual, ldres, T))
+    return FA4_ERR_INVALID_ARG;
   a.fused = true;
   a.dtype = dtype;
   a.T = T;
@@ -694,6 +706,14 @@ fa4_status fa4_dropout_add_layernorm_bwd(const void *dy, int64_t lddy, const voi
       (e = make_drop(p, seed, step, &a.drop)) != FA4_OK ||
       (e = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
     return e;
+  if (dx == dres) return FA4_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    const void *out = i ? dres : dx;
+    const int64_t ld = i ? lddres : lddx;
+    if (other_rows(out, ld, dy, lddy, T) || other_rows(out, ld, s, lds, T) ||
+        other_rows(out, ld, ds, ldds, T))
+      return FA4_ERR_INVALID_ARG;
+  }
   a.fused = true;
   a.dtype = dtype;
   a.T = T;
@@ -727,6 +747,7 @@ fa4_status fa4_swiglu_bwd(const void *z, int64_t ldz, const void *dh, int64_t ld
       lddh % 8)
     return FA4_ERR_SHAPE;
   if (!aligned16(z) || !aligned16(dh) || !aligned16(dz)) return FA4_ERR_ALIGN;
+  if (dz == dh || other_rows(dz, lddz, z, ldz, T)) return FA4_ERR_INVALID_ARG;
   const fa4::SwigluBwdArgs a = {static_cast<const uint16_t *>(z), static_cast<const uint16_t *>(dh),
                                 static_cast<uint16_t *>(dz), T, F, ldz, lddh, lddz};
   return cuda_status(fa4::launch_swiglu_bwd(a, S(stream)));

@@ -102,6 +102,27 @@ def test_c_calls_reject_bad_arguments(call, cases):
         assert call(**case) == expect, case
 
 
+OUT = DEV + (1 << 20)
+
+
+@pytest.mark.parametrize("call,cases", [
+    (norm_fwd, [dict(ldy=72), dict(ldx=72)]),
+    (norm_bwd, [dict(dy=OUT, lddx=72), dict(x=OUT, lddx=72),
+                dict(dy=OUT, x=OUT, dres=DEV, lddres=72)]),
+    (drop_fwd, [dict(ldy=72), dict(x=OUT, res=DEV, ldres=72)]),
+    (drop_bwd, [dict(ldy=72)]),
+    (fused_fwd, [dict(), dict(s=OUT, ldy=72), dict(y=OUT, lds=72), dict(s=OUT, res=OUT, lds=72)]),
+    (fused_bwd, [dict(), dict(dres=OUT, lddx=72), dict(dx=OUT, lddres=72),
+                 dict(dx=OUT, dy=OUT, s=OUT, lddres=72)]),
+    (swiglu_bwd, [dict(z=OUT), dict(dh=OUT, lddz=136)]),
+], ids=["norm_fwd", "norm_bwd", "drop_fwd", "drop_bwd", "fused_fwd", "fused_bwd", "swiglu_bwd"])
+def test_outputs_in_place_keep_their_inputs_rows(call, cases):
+    """The same address under another leading dimension, and one matrix for
+    two outputs."""
+    for case in cases:
+        assert call(**case) == 1, case
+
+
 def test_workspace_sizes():
     n = ctypes.c_size_t()
     L = fa.lib()
