@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   T *dres = FUSED ? static_cast<T *>(p.dres) + q * p.lddres + col : nullptr;
 
   const int parts = CLUSTER ? g.cluster * g.warps : g.warps;  // of a row's sums
-  cp_async_wait(g.stages > 1 ? g.stages - 2 : 0);             // the oldest group holds the weight
+  if (g.stages == 1) cp_async_commit();            // no row has been asked for: the weight's copies alone
+  cp_async_wait(g.stages > 1 ? g.stages - 2 : 0);  // the oldest group holds the weight
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < CH; ++j) read_vec<T, W>(wsm + warp * CH * kTile + j * kTile, lane, w[j]);

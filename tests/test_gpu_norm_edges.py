@@ -1,0 +1,46 @@
+"""Layer norm backward where its launch has borders of its own: rows for which
+one stage of the ring is all that fits.  Bounds as in rows_ref.py."""
+import pytest
+import torch
+
+import fp4_quantization_block_b200 as fa
+import rows_ref as R
+from gpu_util import need_gpu
+from test_gpu_norm import EPS, SEED, check_bwd, cpu, held
+
+pytestmark = pytest.mark.gpu
+
+
+def one_stage_inputs(T, N, pad):
+    g = torch.Generator().manual_seed(T * 7 + N)
+    mats = [held(torch.randn(T, N, generator=g) + m, torch.float32, pad) for m in (0.5, 0.0, 0.0)]
+    # a weight that is nowhere what it is 4, 128 or 256 columns away
+    w = (torch.randn(N, generator=g) * torch.logspace(-1, 1, N)).cuda()
+    return mats, w
+
+
+def cold_l2():
+    torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(1)
+
+
+@pytest.mark.parametrize("T,N,pad", [(40, 7681, 0), (40, 8191, 0), (40, 8192, 4), (17, 8192, 3),
+                                     (1000, 8191, 0), (20, 15361, 0), (20, 16383, 0), (9, 30721, 0),
+                                     (9, 32767, 0), (3, 61441, 0), (3, 65535, 0)], ids=lambda v: str(v))
+@pytest.mark.parametrize("center", [True, False], ids=["layer", "rms"])
+def test_backward_with_a_ring_of_one_stage(T, N, pad, center):
+    """binary32 rows off 16-byte boundaries with a residual gradient fill the
+    shared memory with one row's columns: the staged weight must have arrived
+    all the same, in the plain and in the fused call."""
+    need_gpu()
+    (x, dy, ds), w = one_stage_inputs(T, N, pad)
+    _, mean, rstd = fa.layer_norm_fwd(x, w, None, EPS, center=center)
+    cold_l2()
+    dx, dw, db = fa.layer_norm_bwd(dy, x, w, mean, rstd, center=center, dres=ds)
+    check_bwd(dy, x, w, mean, rstd, center, ds, dx, dw, db)
+    cold_l2()
+    dx2, dres, dw2, db2 = fa.dropout_add_layer_norm_bwd(dy, ds, x, w, mean, rstd, 0.25, SEED, center=center)
+    check_bwd(dy, x, w, mean, rstd, center, ds, dres, dw2, db2)
+    mask = (fa.dropout_fwd(torch.ones_like(dx), 0.25, SEED) != 0).cpu()
+    (full, _, _), (bound, _, _) = R.norm_bwd(*cpu(dy, x, w, mean, rstd), center, ds.cpu())
+    want, b3 = R.drop(full, mask, 1 / 0.75)
+    R.check("dx", dx2, want, torch.where(mask, bound / 0.75, 0.0) + b3, torch.float32)
