@@ -82,9 +82,12 @@ inline Drop make_drop(const DropArgs &d) { return {d.seed, d.step, d.threshold, 
 
 template <typename K, typename P>
 cudaError_t launch_rows(K kern, const P &p, const Layout &g, size_t smem, int ctas, cudaStream_t st) {
+  // The limit belongs to the kernel, not to the launch: every call sets the
+  // same one, so that a call from another thread, for other rows, cannot lower
+  // it between here and the launch.
   if (smem > 40 * 1024) {  // static shared memory counts towards the default 48 KB too
     const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -1,12 +1,15 @@
-"""Layer norm backward where its launch has borders of its own: rows for which
-one stage of the ring is all that fits.  Bounds as in rows_ref.py."""
+"""Layer norm where its launch has borders of its own: rows for which one stage
+of the ring is all that fits, calls from several host threads at once.  Bounds
+as in rows_ref.py."""
+import threading
+
 import pytest
 import torch
 
 import fp4_quantization_block_b200 as fa
 import rows_ref as R
 from gpu_util import need_gpu
-from test_gpu_norm import EPS, SEED, check_bwd, cpu, held
+from test_gpu_norm import EPS, SEED, check_bwd, cpu, held, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +47,46 @@ def test_backward_with_a_ring_of_one_stage(T, N, pad, center):
     (full, _, _), (bound, _, _) = R.norm_bwd(*cpu(dy, x, w, mean, rstd), center, ds.cpu())
     want, b3 = R.drop(full, mask, 1 / 0.75)
     R.check("dx", dx2, want, torch.where(mask, bound / 0.75, 0.0) + b3, torch.float32)
+
+
+@pytest.mark.parametrize("backward", [False, True], ids=["fwd", "bwd"])
+def test_host_threads_with_rows_of_different_lengths(backward):
+    """C calls of one kernel that need different amounts of shared memory, from
+    four threads at once, each on a stream of its own: none is refused, and
+    each gives what it gives alone."""
+    need_gpu()
+    L, T = fa.lib(), 40
+    sets = []
+    for N in (4096, 8192, 6144, 2048):
+        (x, _, dy, ds), w, b = inputs(T, N, torch.bfloat16, seed=N)
+        y, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+        want = (y,) if not backward else fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)
+        got = [torch.zeros_like(t) for t in want]
+        ws = fa.workspace(fa.layer_norm_ws_bytes(T, N))
+        st = torch.cuda.Stream()
+        p = [t.data_ptr() for t in (x, dy, ds, w, b, mean, rstd, *got)]
+        if backward:
+            args = (p[1], N, p[0], N, p[2], N, T, N, 0, p[3], 0, 1, p[5], p[6], p[7], N, p[8], p[9],
+                    ws.data_ptr(), ws.numel(), st.cuda_stream)
+        else:
+            args = (p[0], N, T, N, 0, p[3], p[4], 0, EPS, 1, p[7], N, p[5], p[6], st.cuda_stream)
+        sets.append((args, got, want, (x, dy, ds, w, b, mean, rstd, ws, st)))
+    torch.cuda.synchronize()
+    call = L.fa4_layernorm_bwd if backward else L.fa4_layernorm_fwd
+    start, refused = threading.Barrier(len(sets)), [0] * len(sets)
+
+    def work(k):
+        args = sets[k][0]
+        start.wait()
+        for _ in range(10000):
+            refused[k] += call(*args) != 0
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(sets)
+    for _, got, want, _ in sets:
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
