@@ -98,6 +98,7 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
         "fa4_debug_nv_block_scale": [P, f32, i64, P, P, P],
         "fa4_debug_silu": [P, i64, P, P],
         "fa4_debug_gemm_timeout": [_QT, _QT, i64, i64, i64, ci, P, i64, ci, u64, P, sz, P],
+        "fa4_debug_layernorm_bwd_timeout": [P, P, i64, i64, P, P, P, P, P, P, i64, u64, P, sz, P],
         "fa4_quantize_nvfp4_global_noalloc": [P, i64, i64, i64, ci, ci, u64, _QT, P],
         "fa4_swiglu_quantize": [P, i64, i64, i64, ci, ci, u64, _QT, ci, ci, u32, ci, u64, _QT, P],
         "fa4_swiglu_bwd": [P, i64, P, i64, i64, i64, P, i64, P],
@@ -733,7 +734,9 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     """(dx, dweight, dbias): dx of layer_norm_fwd plus dres, the gradient that
     reaches x by another way (the residual stream); dweight and dbias are
     float32 sums over the rows in a fixed order (dbias None without
-    bias_grad)."""
+    bias_grad).  A wait between CTAs that runs out (wide rows; 2 s) leaves NaN
+    in what it did not compute, and its status in ws, if that was zeroed
+    (workspace, check_device_status)."""
     ldx, lddy = _rows(x, "x"), _rows(dy, "dy", x)
     if _elsewhere(x):
         with torch.cuda.device(x.device):
@@ -864,3 +867,22 @@ def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = Non
     _check(lib().fa4_swiglu_bwd(_ptr(z), ldz, _ptr(dh), lddh, T, F2 // 2, _ptr(out), out.stride(0),
                                 _stream_of(z)), "fa4_swiglu_bwd")
     return out
+
+
+def debug_layer_norm_bwd_timeout(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                                 mean: torch.Tensor, rstd: torch.Tensor, withheld_row: int,
+                                 timeout_ns: int, ws: torch.Tensor
+                                 ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """layer_norm_bwd of contiguous bf16 rows whose waits between CTAs end
+    after timeout_ns, one CTA keeping its sums of withheld_row to itself."""
+    for t, n, shape, dtype in ((dy, "dy", x.shape, torch.bfloat16), (x, "x", x.shape, torch.bfloat16),
+                               (weight, "weight", x.shape[1:], torch.bfloat16),
+                               (mean, "mean", x.shape[:1], torch.float32),
+                               (rstd, "rstd", x.shape[:1], torch.float32)):
+        _check_out(t, shape, (dtype,), x.device, n)
+    dx, dweight, dbias = torch.empty_like(x), _new_f32(x, x.shape[1]), _new_f32(x, x.shape[1])
+    _check(lib().fa4_debug_layernorm_bwd_timeout(_ptr(dy), _ptr(x), *x.shape, _ptr(weight), _ptr(mean),
+                                                 _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                                 withheld_row, timeout_ns, _ptr(ws), ws.numel(),
+                                                 _stream(x.device)), "fa4_debug_layernorm_bwd_timeout")
+    return dx, dweight, dbias

@@ -256,6 +256,50 @@ fa4_status check_norm_bwd_out(int64_t T, int64_t N, const float *dw, const float
   return aligned16(ws) ? FA4_OK : FA4_ERR_ALIGN;
 }
 
+// Checks and arguments of a layer norm's backward pass.
+fa4_status norm_bwd_args(const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *dres,
+                         int64_t lddres, int64_t T, int64_t N, int dtype, const void *weight, int w_dtype,
+                         int center, const float *mean, const float *rstd, void *dx, int64_t lddx,
+                         float *dweight, float *dbias, void *workspace, size_t workspace_bytes,
+                         fa4::NormBwdArgs *out) {
+  if (!dtype_ok(dtype)) return FA4_ERR_INVALID_ARG;
+  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
+  fa4_status s = check_rows(dy, lddy, N, dtype);
+  if (s != FA4_OK || (s = check_rows(x, ldx, N, dtype)) != FA4_OK ||
+      (dres && (s = check_rows(dres, lddres, N, dtype)) != FA4_OK) ||
+      (s = check_rows(dx, lddx, N, dtype)) != FA4_OK ||
+      (s = check_weights(weight, nullptr, w_dtype, dtype)) != FA4_OK ||
+      (s = check_stats(mean, rstd, center)) != FA4_OK ||
+      (s = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
+    return s;
+  if (other_rows(dx, lddx, dy, lddy, T) || other_rows(dx, lddx, x, ldx, T) ||
+      other_rows(dx, lddx, dres, lddres, T))
+    return FA4_ERR_INVALID_ARG;
+  fa4::NormBwdArgs &a = *out;
+  a.fused = false;
+  a.dtype = dtype;
+  a.T = T;
+  a.N = N;
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.ds = dres;
+  a.ldds = lddres;
+  a.w = weight;
+  a.w_f32 = w_dtype == FA4_FP32;
+  a.center = center;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dw = dweight;
+  a.db = dbias;
+  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
+  a.status = static_cast<uint32_t *>(workspace);
+  return FA4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -577,42 +621,10 @@ fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x, int64_
                              const void *weight, fa4_dtype w_dtype, int center, const float *mean,
                              const float *rstd, void *dx, int64_t lddx, float *dweight, float *dbias,
                              void *workspace, size_t workspace_bytes, void *stream) {
-  if (!dtype_ok(dtype)) return FA4_ERR_INVALID_ARG;
-  if (!rows_shape_ok(T, N)) return FA4_ERR_SHAPE;
-  fa4_status s = check_rows(dy, lddy, N, dtype);
-  if (s != FA4_OK || (s = check_rows(x, ldx, N, dtype)) != FA4_OK ||
-      (dres && (s = check_rows(dres, lddres, N, dtype)) != FA4_OK) ||
-      (s = check_rows(dx, lddx, N, dtype)) != FA4_OK ||
-      (s = check_weights(weight, nullptr, w_dtype, dtype)) != FA4_OK ||
-      (s = check_stats(mean, rstd, center)) != FA4_OK ||
-      (s = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
-    return s;
-  if (other_rows(dx, lddx, dy, lddy, T) || other_rows(dx, lddx, x, ldx, T) ||
-      other_rows(dx, lddx, dres, lddres, T))
-    return FA4_ERR_INVALID_ARG;
   fa4::NormBwdArgs a = {};
-  a.fused = false;
-  a.dtype = dtype;
-  a.T = T;
-  a.N = N;
-  a.dy = dy;
-  a.lddy = lddy;
-  a.x = x;
-  a.ldx = ldx;
-  a.ds = dres;
-  a.ldds = lddres;
-  a.w = weight;
-  a.w_f32 = w_dtype == FA4_FP32;
-  a.center = center;
-  a.mean = mean;
-  a.rstd = rstd;
-  a.dx = dx;
-  a.lddx = lddx;
-  a.dw = dweight;
-  a.db = dbias;
-  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kHdr);
-  a.status = static_cast<uint32_t *>(workspace);
-  return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
+  const fa4_status s = norm_bwd_args(dy, lddy, x, ldx, dres, lddres, T, N, dtype, weight, w_dtype, center, mean,
+                                     rstd, dx, lddx, dweight, dbias, workspace, workspace_bytes, &a);
+  return s != FA4_OK ? s : cuda_status(fa4::launch_norm_bwd(a, S(stream)));
 }
 
 fa4_status fa4_dropout_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldres, int64_t T,
@@ -802,6 +814,22 @@ fa4_status fa4_debug_gemm_timeout(fa4_qtensor A, fa4_qtensor B, int64_t M, int64
   if (timeout_ns == 0 || timeout_ns > kDefaultTimeoutNs) return FA4_ERR_INVALID_ARG;
   return do_gemm(A, B, M, N, K, fmt, 1.0f, D, ldd, FA4_OUT_FP32, static_cast<uint8_t *>(workspace),
                  S(stream), skip_k_tile, timeout_ns);
+}
+
+fa4_status fa4_debug_layernorm_bwd_timeout(const void *dy, const void *x, int64_t T, int64_t N,
+                                           const void *weight, const float *mean, const float *rstd,
+                                           void *dx, float *dweight, float *dbias, int64_t withheld_row,
+                                           uint64_t timeout_ns, void *workspace, size_t workspace_bytes,
+                                           void *stream) {
+  fa4::NormBwdArgs a = {};
+  const fa4_status s = norm_bwd_args(dy, N, x, N, nullptr, 0, T, N, FA4_BF16, weight, FA4_BF16, 1, mean, rstd,
+                                     dx, N, dweight, dbias, workspace, workspace_bytes, &a);
+  if (s != FA4_OK) return s;
+  if (timeout_ns == 0 || timeout_ns > kDefaultTimeoutNs || withheld_row < -1 || withheld_row >= T)
+    return FA4_ERR_INVALID_ARG;
+  a.timeout_ns = timeout_ns;
+  a.withheld = withheld_row;
+  return cuda_status(fa4::launch_norm_bwd(a, S(stream)));
 }
 
 }  // extern "C"

@@ -128,6 +128,8 @@ struct NormBwdArgs {
   float *dw, *db;
   float *partials;  // norm_partials_count(T, N) * 2 * N
   uint32_t *status;  // bounded-wait status word
+  uint64_t timeout_ns = 2000000000ull;
+  int64_t withheld = -1;  // diagnostics: a row whose sums one CTA of its cluster keeps to itself
   DropArgs drop;
 };
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, cudaStream_t st);

@@ -17,6 +17,8 @@ struct BwdParams {
   float *partials;  // [cluster][2][N]
   float *dw, *db;   // where there is one cluster only
   uint32_t *status;  // set when a wait within a cluster gives up
+  uint64_t timeout_ns;  // the limit of such a wait
+  uint32_t withheld;    // a row whose sums a cluster's first CTA does not send; no row is ~0
   int one;
   Drop drop;
   int64_t step_x, step_dy, step_ds, step_dx, step_dres;  // elements between a team's rows
@@ -107,6 +109,20 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(const BwdParams p) {
   }
 }
 
+// The columns col .. end - 1 of dx (and dres) of n of a warp's rows, all NaN.
+// Out of line: inside the kernel its loops cost registers of the loop over the
+// rows (fused 2000 x 24576 bf16: 180 us against 133).
+template <typename T, bool FUSED>
+__device__ __noinline__ void leave_nan(void *dx, int64_t lddx, void *dres, int64_t lddres, int64_t row,
+                                       uint32_t step, int n, int col, int end) {
+  const T nan = from_float<T>(__int_as_float(0x7FC00000));
+  for (; n > 0; --n, row += step)
+    for (int c = col + (threadIdx.x & 31); c < end; c += 32) {
+      static_cast<T *>(dx)[row * lddx + c] = nan;
+      if constexpr (FUSED) static_cast<T *>(dres)[row * lddres + c] = nan;
+    }
+}
+
 // dx of a team's rows; dw and db of its columns stay in registers over its
 // rows, are added up over the CTA's teams in order and go to the CTA's partial
 // sums.  A row takes two passes over its columns, with mean(g) and mean(g xh)
@@ -117,7 +133,9 @@ __global__ void __launch_bounds__(256) norm_dw_wide_kernel(const BwdParams p) {
 // parts of its row, not for another team or for a fence over its stores.  Two
 // barriers and two buffers take turns: a part of the row after the next one is
 // sent only when all parts of the next one have come, and a warp sends its own
-// only after it has read this row's.
+// only after it has read this row's.  A wait that gives up ends its
+// warp's rows: the status word is set, and what the warp leaves undone is NaN,
+// its columns of dx (and dres) from that row on, and of dw and db.
 //
 // 8192 x 4096 bf16 with ds takes 47.8 us (5.6 TB/s; 65536 rows 7.0 TB/s):
 // nearly 10 us are a launch's own, the first row's latency, the last row's,
@@ -218,7 +236,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
   for (int j = 0; j < CH; ++j) read_vec<T, W>(wsm + warp * CH * kTile + j * kTile, lane, w[j]);
   float2 *red0 = &red[0][team * parts], *red1 = &red[1][team * parts];
   const bool upper = lane >= 16;  // the lanes that add up the second sum
-  int ts = 0;
+  int ts = 0, stop = n;  // the row whose wait gave up
   uint32_t row = q;
   for (int k = 0; k < n; ++k) {
     __syncwarp();  // the stage filled next was read by the whole warp
@@ -277,10 +295,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
         uint64_t *const barrier = &arrived[k & 1][team];
         const float2 both = make_float2(__shfl_sync(0xFFFFFFFFu, v, 0), __shfl_sync(0xFFFFFFFFu, v, 16));
         if (warp == 0 && lane == 0) barrier_expect(barrier, 8 * parts);
-        if (lane < g.cluster) cluster_send(&red0[rank * g.warps + warp], barrier, lane, both);
+        if (lane < g.cluster && !(row == p.withheld && rank == 0))
+          cluster_send(&red0[rank * g.warps + warp], barrier, lane, both);
         // (a wait ends by itself; what a lane saw decides for the warp)
-        if (!__all_sync(0xFFFFFFFFu, barrier_wait(barrier, (k >> 1) & 1))) {
-          if (lane == 0) *p.status = 7u;
+        if (!__all_sync(0xFFFFFFFFu, barrier_wait(barrier, (k >> 1) & 1, p.timeout_ns))) {
+          stop = k;
           break;
         }
         v = 0.0f;
@@ -333,9 +352,23 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 1) norm_bwd_kernel(const BwdPa
     ts = ts + kStage == ring_len ? 0 : ts + kStage;
   }
 
-  if constexpr (CLUSTER) {  // nobody leaves while something may still be sent to them
+  if constexpr (CLUSTER) {
+    if (stop < n) {
+      if (lane == 0) *p.status = 7u;
+      leave_nan<T, FUSED>(p.dx, p.lddx, p.dres, p.lddres, row, g.step, n - stop, col,
+                          (int)p.N - col < CH * kTile ? (int)p.N : col + CH * kTile);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = f2_set(__int_as_float(0x7FC00000));
+    }
+    // nobody leaves while something may still be sent to them, or (where a
+    // wait gave up) may be on its way
     __syncwarp();
     cluster_sync();
+    if (stop < n)
+      for (const uint64_t begin = globaltimer(); globaltimer() - begin < 100000ull;) __nanosleep(1000);
+    __syncwarp();
   }
   // the teams' sums, through the ring's memory, in the teams' order
   float *const out_w = p.one ? p.dw : p.partials + (int64_t)cid * 2 * p.N;
@@ -444,6 +477,8 @@ cudaError_t backward_w(const NormBwdArgs &a, int *n, cudaStream_t st) {
   p.partials = a.partials;
   p.dw = a.dw;
   p.status = a.status;
+  p.timeout_ns = a.timeout_ns;
+  p.withheld = a.withheld < 0 ? ~0u : (uint32_t)a.withheld;
   p.db = a.db;
   p.drop = make_drop(a.drop);
   auto go = [&](auto v, auto f) {

@@ -477,10 +477,15 @@ __device__ __forceinline__ void barrier_expect(uint64_t *barrier, int bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(barrier)), "r"(bytes)
                : "memory");
 }
-// Waits for a phase; false if it did not complete within some seconds.
-__device__ __forceinline__ bool barrier_wait(uint64_t *barrier, uint32_t parity) {
+__device__ __forceinline__ uint64_t globaltimer() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for a phase; false if it did not complete within timeout_ns.
+__device__ __forceinline__ bool barrier_wait(uint64_t *barrier, uint32_t parity, uint64_t timeout_ns) {
   const uint32_t addr = smem_addr(barrier);
-  uint64_t begin = 0, now;
+  uint64_t begin = 0;
   for (uint32_t i = 0;; ++i) {
     uint32_t done;
     asm volatile(
@@ -491,10 +496,10 @@ __device__ __forceinline__ bool barrier_wait(uint64_t *barrier, uint32_t parity)
         : "r"(addr), "r"(parity)
         : "memory");
     if (done) return true;
-    if ((i & 255u) == 255u) {
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if ((i & 15u) == 15u) {
+      const uint64_t now = globaltimer();
       if (begin == 0) begin = now;
-      if (now - begin > 2000000000ull) return false;
+      if (now - begin > timeout_ns) return false;
     }
   }
 }

@@ -375,8 +375,9 @@ FA4_API fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int6
  * a call repeats bit for bit.  dx may be dy, x or dres itself (same leading
  * dimension).  Workspace: fa4_layernorm_ws_bytes (nothing in it has to be
  * zero); calls that may run at the same time need one each.  A bounded wait
- * that gives up (rows shared by a cluster) sets the header's status word and
- * leaves the outputs incomplete: zero the header first to read it with
+ * that gives up (rows shared by a cluster; 2 s) sets the header's status word,
+ * and what it left undone is NaN: its rows of dx from the one that it waited
+ * for on, dweight and dbias.  Zero the header first to read the status with
  * fa4_check_device_status.
  * Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED (w_dtype), WORKSPACE, CUDA. */
 FA4_API fa4_status fa4_layernorm_ws_bytes(int64_t T, int64_t N, size_t *workspace_bytes);
@@ -500,6 +501,19 @@ FA4_API fa4_status fa4_debug_gemm_timeout(fa4_qtensor A, fa4_qtensor B, int64_t 
                                   fa4_format fmt, void *D, int64_t ldd, int skip_k_tile,
                                   uint64_t timeout_ns, void *workspace, size_t workspace_bytes,
                                   void *stream);
+
+/* The same for rows that a cluster shares: fa4_layernorm_bwd (bf16, weight
+ * too, contiguous rows, centred, no dres) with every wait limited to
+ * timeout_ns (0 < timeout_ns <= 2 s) and, when withheld_row >= 0, a cluster
+ * whose first CTA keeps its sums of that row to itself, so that the waits of
+ * all its CTAs must run out.  Rows that no cluster shares (as many columns as
+ * one CTA holds, or more than a cluster) wait for nothing. */
+FA4_API fa4_status fa4_debug_layernorm_bwd_timeout(const void *dy, const void *x, int64_t T, int64_t N,
+                                                   const void *weight, const float *mean,
+                                                   const float *rstd, void *dx, float *dweight,
+                                                   float *dbias, int64_t withheld_row,
+                                                   uint64_t timeout_ns, void *workspace,
+                                                   size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

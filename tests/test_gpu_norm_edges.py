@@ -1,6 +1,6 @@
 """Layer norm where its launch has borders of its own: rows for which one stage
-of the ring is all that fits, calls from several host threads at once.  Bounds
-as in rows_ref.py."""
+of the ring is all that fits, calls from several host threads at once, waits
+between CTAs that run out.  Bounds as in rows_ref.py."""
 import threading
 
 import pytest
@@ -90,3 +90,36 @@ def test_host_threads_with_rows_of_different_lengths(backward):
     assert refused == [0] * len(sets)
     for _, got, want, _ in sets:
         assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
+# (T, N, a row, the rows that its team takes from it on): clusters of four, of
+# two and of eight, one team each, and one cluster of eight for a few rows
+LEFT = [(100, 20000, 5, [5, 38, 71]), (100, 20000, 99, [99]), (200, 12288, 73, [73, 147]),
+        (40, 65536, 17, [17, 32]), (6, 4096, 2, [2])]
+
+
+@pytest.mark.parametrize("T,N,row,left", LEFT, ids=[f"{c[0]}x{c[1]}-{c[2]}" for c in LEFT])
+def test_a_wait_that_runs_out_is_seen_in_the_outputs_and_in_the_status(T, N, row, left):
+    """One CTA keeps its sums of one row to itself: the waits of its cluster end
+    after 20 ms, dx of the rows left undone and the sums over the rows are NaN,
+    the other rows are as they always are, the status says so, and the next call
+    on the same workspace is right."""
+    need_gpu()
+    (x, _, dy, _), w, b = inputs(T, N, torch.bfloat16, seed=T)
+    _, mean, rstd = fa.layer_norm_fwd(x, w, b, EPS)
+    want = fa.layer_norm_bwd(dy, x, w, mean, rstd)
+    ws = fa.workspace(fa.layer_norm_ws_bytes(T, N))
+    same = fa.debug_layer_norm_bwd_timeout(dy, x, w, mean, rstd, -1, 1_000_000_000, ws)
+    assert fa.check_device_status(ws) == 0
+    assert all(torch.equal(a, c) for a, c in zip(same, want))
+    dx, dw, db = fa.debug_layer_norm_bwd_timeout(dy, x, w, mean, rstd, row, 20_000_000, ws)
+    assert fa.check_device_status(ws) == 7
+    assert fa.check_device_status(ws) == 0  # read clears it
+    undone = torch.zeros(T, dtype=torch.bool, device="cuda")
+    undone[left] = True
+    assert torch.isnan(dx[undone]).all()
+    assert torch.equal(dx[~undone], want[0][~undone])
+    assert torch.isnan(dw).all() and torch.isnan(db).all()
+    again = fa.layer_norm_bwd(dy, x, w, mean, rstd, ws=ws)
+    assert fa.check_device_status(ws) == 0
+    assert all(torch.equal(a, c) for a, c in zip(again, want))

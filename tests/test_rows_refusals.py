@@ -191,3 +191,16 @@ def test_bindings_refuse_mismatched_operands():
                  lambda: fa.dropout_fwd(x[:0], 0.1, 1)):
         with pytest.raises(fa.FA4Error):
             call()
+
+
+def test_the_diagnostic_of_the_cluster_waits_refuses_bad_limits_and_rows():
+    def call(**k):
+        a = dict(dy=DEV, x=DEV, T=4, N=64, w=DEV, mean=DEV, rstd=DEV, dx=DEV, dw=DEV, db=DEV, row=-1, ns=1000,
+                 ws=DEV, wsb=1 << 24)
+        a.update(k)
+        return fa.lib().fa4_debug_layernorm_bwd_timeout(*a.values(), None)
+
+    for case, expect in [(dict(ns=0), 1), (dict(ns=2_000_000_001), 1), (dict(row=4), 1), (dict(row=-2), 1),
+                         (dict(x=None), 1), (dict(mean=None), 1), (dict(T=0), 2), (dict(ws=None), 5),
+                         (dict(wsb=300), 5), (dict(dx=DEV + 1), 3)]:
+        assert call(**case) == expect, case
