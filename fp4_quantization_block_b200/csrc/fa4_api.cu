@@ -272,7 +272,7 @@ fa4_status norm_bwd_args(const void *dy, int64_t lddy, const void *x, int64_t ld
       (s = check_stats(mean, rstd, center)) != FA4_OK ||
       (s = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
     return s;
-  if (other_rows(dx, lddx, dy, lddy, T) || other_rows(dx, lddx, x, ldx, T) ||
+  if (dweight == dbias || other_rows(dx, lddx, dy, lddy, T) || other_rows(dx, lddx, x, ldx, T) ||
       other_rows(dx, lddx, dres, lddres, T))
     return FA4_ERR_INVALID_ARG;
   fa4::NormBwdArgs &a = *out;
@@ -589,7 +589,7 @@ fa4_status fa4_layernorm_fwd(const void *x, int64_t ldx, int64_t T, int64_t N, f
       (s = check_weights(weight, bias, w_dtype, dtype)) != FA4_OK ||
       (s = check_stats(mean, rstd, center)) != FA4_OK)
     return s;
-  if (other_rows(y, ldy, x, ldx, T)) return FA4_ERR_INVALID_ARG;
+  if (mean == rstd || other_rows(y, ldy, x, ldx, T)) return FA4_ERR_INVALID_ARG;
   fa4::NormFwdArgs a = {};
   a.fused = false;
   a.dtype = dtype;
@@ -673,7 +673,7 @@ fa4_status fa4_dropout_add_layernorm_fwd(const void *x, int64_t ldx, const void 
       (e = check_stats(mean, rstd, center)) != FA4_OK ||
       (e = make_drop(p, seed, step, &a.drop)) != FA4_OK)
     return e;
-  if (y == s || other_rows(y, ldy, x, ldx, T) || other_rows(y, ldy, residual, ldres, T) ||
+  if (y == s || mean == rstd || other_rows(y, ldy, x, ldx, T) || other_rows(y, ldy, residual, ldres, T) ||
       other_rows(s, lds, x, ldx, T) || other_rows(s, lds, residual, ldres, T))
     return FA4_ERR_INVALID_ARG;
   a.fused = true;
@@ -718,7 +718,7 @@ fa4_status fa4_dropout_add_layernorm_bwd(const void *dy, int64_t lddy, const voi
       (e = make_drop(p, seed, step, &a.drop)) != FA4_OK ||
       (e = check_norm_bwd_out(T, N, dweight, dbias, workspace, workspace_bytes)) != FA4_OK)
     return e;
-  if (dx == dres) return FA4_ERR_INVALID_ARG;
+  if (dx == dres || dweight == dbias) return FA4_ERR_INVALID_ARG;
   for (int i = 0; i < 2; ++i) {
     const void *out = i ? dres : dx;
     const int64_t ld = i ? lddres : lddx;

@@ -344,12 +344,12 @@ FA4_API fa4_status fa4_quantize_nvfp4_global_noalloc(const void *x, int64_t rows
  * any leading dimension and any pointer aligned to its element are taken;
  * rows that start on 16-byte boundaries with N a multiple of 8 are the fast
  * ones.  An output that may be an input itself has that input's leading
- * dimension, and two outputs are never one matrix (INVALID_ARG).  `dtype` is
- * the type of every matrix of the call; weight and bias are of w_dtype, which
- * is `dtype` or FA4_FP32.  Arithmetic, statistics and sums are binary32; a
- * value is rounded once, where it is stored.  Non-finite values are allowed
- * and stay within the rows (and, in the gradients of
- * weight and bias, the columns) that depend on them. */
+ * dimension, and two outputs are never one matrix or one vector (INVALID_ARG).
+ * `dtype` is the type of every matrix of the call; weight and bias are of
+ * w_dtype, which is `dtype` or FA4_FP32.  Arithmetic, statistics and sums are
+ * binary32; a value is rounded once, where it is stored.  Non-finite values
+ * are allowed and stay within the rows (and, in the gradients of weight and
+ * bias, the columns) that depend on them. */
 typedef enum { FA4_BF16 = 0, FA4_FP32 = 1, FA4_FP16 = 2 } fa4_dtype;
 
 /* Layer norm.  For each row x of N values:

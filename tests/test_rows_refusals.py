@@ -204,3 +204,14 @@ def test_the_diagnostic_of_the_cluster_waits_refuses_bad_limits_and_rows():
                          (dict(x=None), 1), (dict(mean=None), 1), (dict(T=0), 2), (dict(ws=None), 5),
                          (dict(wsb=300), 5), (dict(dx=DEV + 1), 3)]:
         assert call(**case) == expect, case
+
+
+@pytest.mark.parametrize("call,case", [
+    (norm_fwd, dict(mean=OUT, rstd=OUT)), (fused_fwd, dict(s=OUT, mean=OUT + 64, rstd=OUT + 64)),
+    (norm_bwd, dict(dw=OUT, db=OUT)), (fused_bwd, dict(dres=OUT, dw=OUT + 64, db=OUT + 64)),
+], ids=["norm_fwd", "fused_fwd", "norm_bwd", "fused_bwd"])
+def test_one_vector_for_two_outputs_is_refused(call, case):
+    """Statistics, or sums, that would overwrite one another."""
+    if torch.cuda.is_available():
+        pytest.skip("validation is tested without a GPU")
+    assert call(**case) == 1
