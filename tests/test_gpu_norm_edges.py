@@ -1,6 +1,7 @@
 """Layer norm where its launch has borders of its own: rows for which one stage
 of the ring is all that fits, calls from several host threads at once, waits
-between CTAs that run out.  Bounds as in rows_ref.py."""
+between CTAs that run out, sums over the rows that are exact.  Bounds as in
+rows_ref.py."""
 import threading
 
 import pytest
@@ -9,7 +10,7 @@ import torch
 import fp4_quantization_block_b200 as fa
 import rows_ref as R
 from gpu_util import need_gpu
-from test_gpu_norm import EPS, SEED, check_bwd, cpu, held, inputs
+from test_gpu_norm import EPS, SEED, TYPES, check_bwd, cpu, held, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +124,25 @@ def test_a_wait_that_runs_out_is_seen_in_the_outputs_and_in_the_status(T, N, row
     again = fa.layer_norm_bwd(dy, x, w, mean, rstd, ws=ws)
     assert fa.check_device_status(ws) == 0
     assert all(torch.equal(a, c) for a, c in zip(again, want))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES.values()), ids=list(TYPES))
+@pytest.mark.parametrize("N", [24, 256, 300, 1024, 4096, 4099, 8200, 12288, 40001, 70000])
+def test_sums_over_the_rows_take_every_row_once(N, dtype):
+    """dy, x and the statistics given to the call are whole numbers, so that
+    every term and every sum of dweight and dbias is exact in binary32 in any
+    order (below 2^24), at row counts on both sides of each layout's borders."""
+    need_gpu()
+    counts = [1, 2, 15, 16, 17, 31, 32, 33, 34, 74, 75, 147, 148, 149, 295, 297, 1185, 3553]
+    g = torch.Generator(device="cuda").manual_seed(N)
+    w = torch.ones(N, dtype=dtype, device="cuda")
+    for T in [t for t in counts if t * N <= 16_000_000]:
+        x, dy, ds = (torch.randint(-8, 9, (T, N), generator=g, device="cuda").to(dtype) for _ in range(3))
+        mean = torch.randint(-2, 3, (T,), generator=g, device="cuda").float()
+        rstd = torch.randint(1, 3, (T,), generator=g, device="cuda").float()
+        xh = (x.double() - mean[:, None]) * rstd[:, None]
+        dw, db = (dy.double() * xh).sum(0), dy.double().sum(0)
+        got = fa.layer_norm_bwd(dy, x, w, mean, rstd, dres=ds)[1:] + \
+            fa.dropout_add_layer_norm_bwd(dy, None, x, w, mean, rstd, 0.1, SEED)[2:]
+        for a, b in zip(got, (dw, db, dw, db)):
+            assert torch.equal(a.double(), b), T
