@@ -1,13 +1,15 @@
 """Layer norm where its launch has borders of its own: rows for which one stage
 of the ring is all that fits, calls from several host threads at once, waits
-between CTAs that run out, sums over the rows that are exact.  Bounds as in
-rows_ref.py."""
+between CTAs that run out, sums over the rows that are exact, rows past 2^31
+elements.  Bounds as in rows_ref.py."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 import fp4_quantization_block_b200 as fa
+import oracle as O
 import rows_ref as R
 from gpu_util import need_gpu
 from test_gpu_norm import EPS, SEED, TYPES, check_bwd, cpu, held, inputs
@@ -146,3 +148,32 @@ def test_sums_over_the_rows_take_every_row_once(N, dtype):
             fa.dropout_add_layer_norm_bwd(dy, None, x, w, mean, rstd, 0.1, SEED)[2:]
         for a, b in zip(got, (dw, db, dw, db)):
             assert torch.equal(a.double(), b), T
+
+
+def kept_in_row(r, N, p, seed):
+    words = [O.philox4x32([j, r, 0, R.DROP_TAG], [seed & 0xFFFFFFFF, seed >> 32], 7) for j in range(-(-N // 8))]
+    u = np.asarray(words, dtype=np.uint32).reshape(-1).view(np.uint16)[:N]  # little endian: low half first
+    return torch.from_numpy(u.astype(np.int64) >= round(p * 65536)).cuda()
+
+
+@pytest.mark.parametrize("dtype,N", [(torch.bfloat16, 32768), (torch.bfloat16, 32765), (torch.float32, 32768),
+                                     (torch.float32, 32765)], ids=["bf16", "bf16-odd", "fp32", "fp32-odd"])
+def test_masks_of_rows_past_2_to_the_31_elements(dtype, N):
+    """Whole rows on both sides of that border, the last one too, against the
+    oracle's generator: dropout alone, and the sum that the fused call stores."""
+    need_gpu()
+    T, p = 70000, 0.25
+    one = torch.ones(1, 1, dtype=dtype, device="cuda").expand(T, N)
+    x = one.contiguous()
+    y = fa.dropout_fwd(x, p, SEED)
+    rows = [0, 1, 2 ** 31 // N, 2 ** 31 // N + 1, T - 1]
+    masks = [kept_in_row(r, N, p, SEED) for r in rows]
+    scale = torch.tensor(1 / 0.75).to(dtype).item()
+    for r, m in zip(rows, masks):
+        assert torch.equal(y[r], torch.where(m, scale, 0.0).to(dtype)), r
+    if dtype == torch.bfloat16:
+        w = torch.ones(N, dtype=dtype, device="cuda")
+        _, s, _, _ = fa.dropout_add_layer_norm_fwd(x, x, w, None, p, SEED, out=y)
+        kept = torch.tensor(1 + 1 / 0.75).to(dtype).item()
+        for r, m in zip(rows, masks):
+            assert torch.equal(s[r], torch.where(m, kept, 1.0).to(dtype)), r
