@@ -763,8 +763,9 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, step: torch.Tensor | None 
     """[residual +] dropout(x) with a mask computed from (seed + step, row,
     column) and never stored; kept values are scaled by the reciprocal of
     their probability (p in steps of 2^-16).  step: one int64 on the device,
-    for graphs that draw a new mask at each replay.  out may be x or
-    residual."""
+    for graphs that draw a new mask at each replay.  Calls of one step (layers,
+    ranks) need seeds further apart than the steps counted, e.g. layer << 32:
+    equal sums are equal masks.  out may be x or residual."""
     ldx = _rows(x, "x")
     if _elsewhere(x):
         with torch.cuda.device(x.device):
@@ -799,8 +800,8 @@ def dropout_add_layer_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: 
                                s: torch.Tensor | None = None
                                ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor | None, torch.Tensor]:
     """(y, s, mean, rstd) in one pass over the data: s = residual + dropout(x)
-    as dropout_fwd gives it, y = the layer norm of the stored s.  s may be
-    residual and out may be x."""
+    as dropout_fwd gives it (with its rule for seeds), y = the layer norm of the
+    stored s.  s may be residual and out may be x."""
     ldx, ldr = _rows(x, "x"), _rows(residual, "residual", x)
     if _elsewhere(x):
         with torch.cuda.device(x.device):

@@ -396,8 +396,12 @@ FA4_API fa4_status fa4_layernorm_bwd(const void *dy, int64_t lddy, const void *x
  * reciprocal of the probability of being kept), 0 where dropped, whatever the
  * dropped value was; plus residual when it is not NULL.  0 <= p < 1.  step is
  * a device pointer to one 64-bit integer or NULL (0): a captured graph draws
- * a new mask at each replay when the caller advances it.  The counters never
- * meet the stochastic rounding's, under any key.  y may be x or residual
+ * a new mask at each replay when the caller advances it.  Equal sums give equal
+ * masks: calls of one step (layers, ranks) need seeds further apart than the
+ * steps that will be counted, e.g. that differ in their high 32 bits (seeds 1
+ * and 2 with steps that count up would give the second call the mask that the
+ * first has a step later).  The counters never meet the stochastic rounding's,
+ * under any key.  y may be x or residual
  * itself (same leading dimension).
  * fa4_dropout_bwd: dx from dy, the same p, seed and *step (the gradient of
  * the residual is dy itself).
