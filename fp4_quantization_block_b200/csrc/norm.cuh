@@ -104,8 +104,8 @@ cudaError_t launch_rows(K kern, const P &p, const Layout &g, size_t smem, int ct
   return cudaLaunchKernelEx(&cfg, kern, p, g);
 }
 
-// The calls for one type of the matrices (norm_bf16.cu, norm_fp16.cu,
-// norm_fp32.cu).  backward: *n partial sums of dw and db are left in
+// The calls for one type of the matrices (norm_fwd_bf16.cu, norm_bwd_bf16.cu
+// and their like for fp16 and fp32).  backward: *n partial sums of dw and db are left in
 // a.partials, none where they are done.
 template <typename T>
 cudaError_t forward(const NormFwdArgs &a, cudaStream_t st);

@@ -1,6 +1,7 @@
-// rows.cuh -- device helpers of the row-wise training operators (norm.cu,
-// dropout.cu): element types, chunks of eight columns, sums over a row's
-// threads, and the dropout mask.
+// rows.cuh -- device helpers of the row-wise training operators (norm_fwd.cuh,
+// norm_bwd.cuh, dropout.cu, swiglu_bwd.cu): element types, chunks of eight
+// columns, sums over a row's threads, the dropout mask, rows kept on the chip,
+// and the exchange between the CTAs of a cluster.
 //
 // A thread's unit is a chunk: eight consecutive columns of one row, which is
 // one 16-byte access of a 16-bit type (two of binary32) and one block of the
