@@ -3,12 +3,13 @@
 //
 // h = silu(g) u, silu(g) = g sg, sg = 1 / (1 + exp(-g)):
 //   du = dh silu(g),   dg = dh u sg (1 + g (1 - sg)),
-// in binary32, each rounded once to bf16.  With e = exp(-|g|) <= 1 the sigmoid
-// and 1 - sg are 1 / (1 + e) and e / (1 + e) in the order of g's sign: neither
-// overflows or cancels, and sg keeps its value for g below -87, where exp(-g)
-// leaves the range that the reciprocal takes.  The reciprocal, of a value
-// between one and two, is the hardware's estimate (one unit in the last place,
-// far inside bf16's step).
+// in binary32, each rounded once to bf16.  The reciprocal is the hardware's
+// estimate (one unit in the last place, far inside bf16's step).  For gates
+// below -87 1 + exp(-g) leaves the range that it takes and sg would be zero, so
+// a thread that has one takes a form of its own, out of line, which leaves the
+// others their 32 registers (8192 x 14336 in a stream of calls 175.5 us, 173.2
+// without the question; one form for all, from exp(-|g|), 179, and on packed
+// pairs, with 38 registers, 183).
 //
 // Bound by memory: 10 bytes per element of h.  8192 x 14336 takes 171 us, 6.85
 // TB/s.  One chunk of eight channels per thread (two or four are as fast there
@@ -34,6 +35,25 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
+// Whether one of eight gates is below -87: as unsigned 16-bit numbers, the
+// negative ones of larger magnitude (NaN among them) are above -87's.
+__device__ __forceinline__ bool any_far(const uint4 &g) {
+  const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(g.x, g.y, g.z), g.w, 0u);
+  return m > 0xC2AEFFFFu || (m << 16) > 0xC2AEFFFFu;
+}
+// A thread's eight channels where any_far, from memory again: below -87 sg is
+// exp(g) to binary32's last bit, the other gates' is what it is beside others.
+__device__ __noinline__ void far_gates(const uint16_t *z, int64_t F, const uint16_t *dh, uint16_t *dz) {
+  using T = __nv_bfloat16;
+  for (int j = 0; j < 8; ++j) {
+    const float g = to_float(reinterpret_cast<const T *>(z)[j]), u = to_float(reinterpret_cast<const T *>(z)[F + j]);
+    const float d = to_float(reinterpret_cast<const T *>(dh)[j]);
+    const float e = expf(g < -87.0f ? g : -g), sg = g < -87.0f ? e : reciprocal(1.0f + e);
+    reinterpret_cast<T *>(dz)[j] = from_float<T>(d * u * (sg * fmaf(g, 1.0f - sg, 1.0f)));
+    reinterpret_cast<T *>(dz)[F + j] = from_float<T>(d * (g * sg));
+  }
+}
+
 // dz may be z itself: a thread reads its elements before it writes them.
 __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArgs p, const int64_t units,
                                                               const Divisor per_row) {
@@ -50,27 +70,25 @@ __global__ void __launch_bounds__(kThreads) swiglu_bwd_kernel(const SwigluBwdArg
   g.v[0] = __ldcs(reinterpret_cast<const uint4 *>(z));
   u.v[0] = __ldcs(reinterpret_cast<const uint4 *>(z + p.F));
   d.v[0] = __ldcs(reinterpret_cast<const uint4 *>(p.dh + row * p.lddh + c));
-  uint64_t gf[4], uf[4], df[4];
+  const bool far = any_far(g.v[0]);
+  float gf[8], uf[8], df[8];
   unpack8(g, gf);
   unpack8(u, uf);
   unpack8(d, df);
-  const uint64_t one = f2_set(1.0f);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float lo = f2_lo(gf[j]), hi = f2_hi(gf[j]);
-    const uint64_t e = f2_pack(expf(-fabsf(lo)), expf(-fabsf(hi))), sum = f2_add(one, e);
-    const float rl = reciprocal(f2_lo(sum)), rh = reciprocal(f2_hi(sum));
-    const uint64_t s = f2_mul(e, f2_pack(rl, rh));
-    const float sl = f2_lo(s), sh = f2_hi(s);
-    const uint64_t sg = f2_pack(lo < 0.0f ? sl : rl, hi < 0.0f ? sh : rh);
-    const uint64_t rest = f2_pack(lo < 0.0f ? rl : sl, hi < 0.0f ? rh : sh);  // 1 - sg
-    const uint64_t du = f2_mul(df[j], f2_mul(gf[j], sg));
-    gf[j] = f2_mul(f2_mul(df[j], uf[j]), f2_mul(sg, f2_fma(gf[j], rest, one)));
+  for (int j = 0; j < 8; ++j) {
+    const float sg = reciprocal(1.0f + expf(-gf[j]));
+    const float du = df[j] * (gf[j] * sg);
+    gf[j] = df[j] * uf[j] * (sg * fmaf(gf[j], 1.0f - sg, 1.0f));
     uf[j] = du;
   }
   pack8(gf, g);
   pack8(uf, u);
   uint16_t *dz = p.dz + row * p.lddz + c;
+  if (far) {  // (nothing of it is stored yet)
+    far_gates(z, p.F, p.dh + row * p.lddh + c, dz);
+    return;
+  }
   *reinterpret_cast<uint4 *>(dz) = g.v[0];
   *reinterpret_cast<uint4 *>(dz + p.F) = u.v[0];
 }

@@ -34,3 +34,21 @@ def test_gates_far_below_zero(dh, up):
                 + f.abs() * 2.0 ** -147 + 2.0 ** -149)
     e_du = b * (gd.abs() * (10 * R.U * sg + 2.0 ** -147) + 2 * R.U * (gd * sg).abs() + 2.0 ** -149)
     R.check("dz", fa.swiglu_bwd(z.cuda(), d.cuda()), want, 2 * torch.cat([e_dg, e_du], 1), torch.bfloat16)
+
+
+def test_ordinary_gates_beside_far_ones():
+    """A channel's result is the same bits whatever its neighbours' gates are,
+    in place too."""
+    need_gpu()
+    g = torch.Generator().manual_seed(0)
+    z = torch.randn(64, 512, generator=g).mul_(4).bfloat16().cuda()
+    dh = torch.randn(64, 256, generator=g).bfloat16().cuda()
+    want = fa.swiglu_bwd(z, dh)
+    far = torch.rand(64, 256, generator=g).cuda() < 0.2
+    z2 = z.clone()
+    z2[:, :256][far] = -95.0
+    got = fa.swiglu_bwd(z2, dh)
+    near = ~far.repeat(1, 2)
+    assert torch.equal(got[near], want[near])
+    fa.swiglu_bwd(z2, dh, out=z2)
+    assert torch.equal(z2, got)
