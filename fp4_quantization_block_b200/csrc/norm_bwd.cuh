@@ -139,10 +139,10 @@ __device__ __noinline__ void leave_nan(void *dx, int64_t lddx, void *dres, int64
 //
 // 8192 x 4096 bf16 with ds takes 47.8 us (5.6 TB/s; 65536 rows 7.0 TB/s):
 // nearly 10 us are a launch's own, the first row's latency, the last row's,
-// the sums at the end and the second launch.  Fused with dropout 68.5 us:
+// the sums at the end and the second launch.  Fused with dropout 68.8 us:
 // half of all issue slots are used, by 16 warps of 128 registers (the sums of
-// dw and db are 32 of them).  Wide rows: 1000 x 14336 fp16 35.0 us, 2.5 TB/s;
-// 2000 x 24576 bf16 91 us (115 with a barrier of the whole cluster at each
+// dw and db are 32 of them).  Wide rows: 1000 x 14336 fp16 34.9 us, 2.5 TB/s;
+// 2000 x 24576 bf16 90 us (115 with a barrier of the whole cluster at each
 // row, which also waits for the stores of dx).  Tried and slower: clusters of
 // two for rows that fit a CTA (50 us at 4096 x 8192 against 45), the second
 // pass computing xh and g again (67 us at 8192 x 4096), four chunks a thread
