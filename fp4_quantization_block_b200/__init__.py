@@ -870,12 +870,15 @@ def swiglu_bwd(z: torch.Tensor, dh: torch.Tensor, out: torch.Tensor | None = Non
     return out
 
 
+@_on_tensor_device
 def debug_layer_norm_bwd_timeout(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                                  mean: torch.Tensor, rstd: torch.Tensor, withheld_row: int,
                                  timeout_ns: int, ws: torch.Tensor
                                  ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """layer_norm_bwd of contiguous bf16 rows whose waits between CTAs end
     after timeout_ns, one CTA keeping its sums of withheld_row to itself."""
+    _rows(x, "x")
+    ws = _norm_ws(ws, x)
     for t, n, shape, dtype in ((dy, "dy", x.shape, torch.bfloat16), (x, "x", x.shape, torch.bfloat16),
                                (weight, "weight", x.shape[1:], torch.bfloat16),
                                (mean, "mean", x.shape[:1], torch.float32),

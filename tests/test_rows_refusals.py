@@ -215,3 +215,9 @@ def test_one_vector_for_two_outputs_is_refused(call, case):
     if torch.cuda.is_available():
         pytest.skip("validation is tested without a GPU")
     assert call(**case) == 1
+
+
+def test_the_diagnostics_binding_refuses_host_tensors():
+    x, w, v = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16), torch.zeros(4)
+    with pytest.raises(ValueError):
+        fa.debug_layer_norm_bwd_timeout(x, x, w, v, v, 0, 1000, torch.zeros(1 << 16, dtype=torch.uint8))
